@@ -69,7 +69,9 @@ typedef enum {
     KVQ_ERR_DIM = -3,     /* D is not 64, 128 or 256                        */
     KVQ_ERR_GROUP = -4,   /* group is not a power of two in [16, D]         */
     KVQ_ERR_COUNT = -5,   /* n_vec < 0 or n_vec > 2^31 - 256                */
-    KVQ_ERR_LAUNCH = -6   /* the kernel launch failed (see kvq_last_cuda_error) */
+    KVQ_ERR_LAUNCH = -6,  /* the kernel launch failed (see kvq_last_cuda_error) */
+    KVQ_ERR_FORMAT = -7   /* paged cache: unknown block size, code format or
+                             element type                                  */
 } kvq_status;
 
 /*
@@ -324,12 +326,140 @@ int kvq_attention_decode_static(const uint16_t *q, const uint8_t *k_packed,
                                 float sm_scale, uint16_t *out, void *stream);
 
 /*
+ * The paged 8-bit cache -- kvq_paged_write, kvq_paged_read,
+ * kvq_paged_attention_decode, kvq_paged_attention_prefill.
+ *
+ * K and V are each kept as 8-bit codes [num_blocks][Hkv][block][D] with one
+ * fp32 scale per (block, KV head), [num_blocks][Hkv]; a code c stands for
+ * c * scale.  block_table [B][max_blocks] places the sequences: position p of
+ * sequence b is slot p % block of the cache block block_table[b][p / block].
+ * Blocks of a sequence lie anywhere and in any order; sequences may share
+ * blocks that none of them writes.
+ *
+ *   dtype    element type of q, k, v and outputs: KVQ_FP16 or KVQ_BF16.
+ *   format   KVQ_INT8: two's-complement codes in [-127, 127]; KVQ_E4M3: OCP
+ *            8-bit floats (4 exponent bits, largest 448; the NaN pattern is
+ *            never written, and reads as +-480 or NaN).
+ *   block    tokens per cache block: 16, 32, 64 or 128.
+ *   D        64, 128 or 256.
+ *   *_stride elements from one token's row [heads][D] to the next; a multiple
+ *            of 8, at least heads * D.
+ * Codes, q, k, v and outputs are 16-byte aligned; tables, lengths and scales
+ * 4-byte.  num_blocks * Hkv * block < 2^31.  Status order: shape (KVQ_ERR_DIM,
+ * KVQ_ERR_FORMAT, KVQ_ERR_COUNT), NULL, alignment.
+ *
+ * Tables and lengths are device memory and are checked on the device: a
+ * position outside its table row or a table entry outside [0, num_blocks) sets
+ * bit 2 of the fault word and its token is skipped (writes), left as it was
+ * (reads) or not attended to; lengths or offsets out of range set bit 3 and
+ * are clamped, or their sequence is skipped.
+ */
+#define KVQ_FP16 0
+#define KVQ_BF16 1
+#define KVQ_INT8 0
+#define KVQ_E4M3 1
+
+/*
+ * kvq_paged_write -- quantise new tokens into the cache as they come, prompts
+ * and single tokens alike.  Sequence b's new tokens are rows cu_tokens[b] ..
+ * cu_tokens[b + 1] - 1 of k and v and take the positions from start[b] on.
+ * For each (block, KV head) that they touch, with a the largest magnitude
+ * among them there:
+ *   s = min(max(a * (1 / Q), 2^-40), 2^40), Q = 127 (int8) or 448 (e4m3);
+ *   S = s if they hold the block's slot 0, else max(old scale, s);
+ *   code = round(x * (1 / S)), to the nearest code, ties to even.
+ * Where S grew, the codes of the slots before the new tokens become
+ * round(code * (old S / S)); slots behind the new tokens keep their codes.
+ * Every operation is an IEEE fp32 one, 1 / Q rounded first; results do not
+ * depend on the launch.
+ * NaN counts as 0; what exceeds Q * 2^40 saturates.
+ *
+ *   k, v        [in]  [n_tokens][Hkv][D], token rows k_stride / v_stride apart.
+ *   cu_tokens   [in]  int32 [B + 1], from 0, not decreasing; rows from
+ *                     cu_tokens[B] on are not read.
+ *   start       [in]  int32 [B], >= 0.
+ * The blocks written in one call are distinct per sequence (two sequences that
+ * write one block race, and leave some mixture of both in it).
+ */
+int kvq_paged_write(const void *k, const void *v, int dtype, int64_t k_stride, int64_t v_stride,
+                    const int32_t *cu_tokens, const int32_t *start, const int32_t *block_table,
+                    int B, int max_blocks, int64_t n_tokens, int Hkv, int D, int block, int format,
+                    int64_t num_blocks, void *k_codes, void *v_codes, float *k_scales,
+                    float *v_scales, void *stream);
+
+/*
+ * kvq_paged_read -- the same tokens back out of the cache: row i of k_out and
+ * v_out (contiguous [n_tokens][Hkv][D]) is code * scale, one fp32 product
+ * rounded to dtype.  Rows from cu_tokens[B] on are left as they were.
+ */
+int kvq_paged_read(const int32_t *cu_tokens, const int32_t *start, const int32_t *block_table,
+                   int B, int max_blocks, int64_t n_tokens, int Hkv, int D, int block, int format,
+                   int64_t num_blocks, const void *k_codes, const void *v_codes,
+                   const float *k_scales, const float *v_scales, int dtype, void *k_out,
+                   void *v_out, void *stream);
+
+/*
+ * kvq_paged_attention_decode -- attention of one token per sequence:
+ *     out[b][h] = sum_t p_t V_t,  p = softmax_t(sm_scale <q[b][h], K_t>),
+ * over the positions t of KV head h / (Hq / Hkv) with t < seq_len[b] and, if
+ * window > 0, t >= seq_len[b] - window (the query is the last of the seq_len
+ * positions; its own key has been written).  No key seen gives zeros.
+ *
+ *   q           [in]  [B][Hq][D], sequences q_stride apart; Hq a multiple of Hkv.
+ *   seq_len     [in]  int32 [B], each in [0, max_blocks * block].
+ *   out         [out] [B][Hq][D], contiguous; must not overlap the inputs.
+ *   workspace   scratch for splitting the key axis; 16-byte aligned, at least
+ *               kvq_paged_workspace_bytes().  With less, or NULL, the call
+ *               runs unsplit: same result up to fp32 summation order, slower.
+ *               Calls that may overlap in time need one each.
+ * The codes enter the products exactly, scores and sums are fp32, the softmax
+ * weights are fp16 values (relative rounding 2^-11) in the value product.
+ * Scales are read as max(scale, 2^-40).
+ */
+int kvq_paged_attention_decode(const void *q, int dtype, int64_t q_stride, const int32_t *seq_len,
+                               const int32_t *block_table, int B, int max_blocks, int Hq, int Hkv,
+                               int D, int block, int format, int64_t num_blocks,
+                               const void *k_codes, const void *v_codes, const float *k_scales,
+                               const float *v_scales, float sm_scale, int window, void *out,
+                               void *workspace, int64_t workspace_bytes, void *stream);
+
+/*
+ * kvq_paged_attention_prefill -- causal attention of any number of new tokens
+ * per sequence.  Sequence b's queries are rows cu_q[b] .. cu_q[b + 1] - 1, n of
+ * them, the j-th at position seq_len[b] - n + j; it sees the keys t up to its
+ * own position and, if window > 0, t > position - window.  A query that sees
+ * none gives zeros; rows from cu_q[B] on are left as they were.
+ *
+ *   q     [in]  [total_q][Hq][D], tokens q_stride apart.
+ *   cu_q  [in]  int32 [B + 1], from 0, not decreasing.
+ *   out   [out] [total_q][Hq][D], contiguous; must not overlap the inputs.
+ * Other arguments and numerics as for kvq_paged_attention_decode.
+ */
+int kvq_paged_attention_prefill(const void *q, int dtype, int64_t q_stride, const int32_t *cu_q,
+                                const int32_t *seq_len, const int32_t *block_table, int B,
+                                int max_blocks, int64_t total_q, int Hq, int Hkv, int D, int block,
+                                int format, int64_t num_blocks, const void *k_codes,
+                                const void *v_codes, const float *k_scales, const float *v_scales,
+                                float sm_scale, int window, void *out, void *workspace,
+                                int64_t workspace_bytes, void *stream);
+
+/*
+ * kvq_paged_workspace_bytes -- bytes of workspace that kvq_paged_attention_decode
+ * (total_q = B) or kvq_paged_attention_prefill uses for these shapes on the
+ * current device, or -1 if the shapes are invalid.  Host-only.
+ */
+int64_t kvq_paged_workspace_bytes(int B, int max_blocks, int64_t total_q, int Hq, int Hkv, int D,
+                                  int block);
+
+/*
  * kvq_fault_status -- the current device's fault word: 0 when every bounded
  * wait of every kernel so far completed; bit 0 set when a quantize,
  * dequantize (base or _ex) or attention warp gave up waiting for its bulk
  * copies (its outputs are then incomplete); bit 1 set by kvq_selftest_wait_timeout; bit 2 set when
- * kvq_quantize_rows skipped an out-of-range row index; bit 3 set when
- * kvq_attention_decode met a sequence length outside [0, T].  Non-zero `clear`
+ * kvq_quantize_rows skipped an out-of-range row index, or a paged call met a
+ * position or block outside its table or cache; bit 3 set when
+ * kvq_attention_decode met a sequence length outside [0, T], or a paged call
+ * lengths or offsets out of range.  Non-zero `clear`
  * resets the word.  Synchronous (it copies the word to the host, which waits
  * for prior work on the device's legacy default stream).  Returns -1 if the
  * word cannot be read.

@@ -16,7 +16,8 @@ PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 SOURCES = [os.path.join(PKG, "csrc", n) for n in ("kvq.cu", "kvq_attn.cu", "kvq_attn_d64.cu", "kvq_attn_d128.cu",
                                                         "kvq_attn_d256.cu", "kvq_ex.cu", "kvq_srft_d64.cu",
-                                                        "kvq_srft_d96.cu", "kvq_srft_d128.cu", "kvq_srft_d256.cu")]
+                                                        "kvq_srft_d96.cu", "kvq_srft_d128.cu", "kvq_srft_d256.cu",
+                                                        "kvq_paged.cu")]
 # Per-unit flags.  The codec units keep --fmad=false: their results are
 # defined bit for bit, and a contracted multiply-add rounds once where the
 # codec's definition rounds twice.  The decode attention is checked against

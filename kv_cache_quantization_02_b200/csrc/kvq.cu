@@ -65,6 +65,9 @@ unsigned int kvq_attn_fault_word(int clear);
 int kvq_attn_last_cuda_error();
 unsigned int kvq_ex_fault_word(int clear);
 int kvq_ex_last_cuda_error();
+// and of the paged 8-bit cache (kvq_paged.cu)
+unsigned int kvq_paged_fault_word(int clear);
+int kvq_paged_last_cuda_error();
 
 namespace {
 
@@ -1408,7 +1411,8 @@ int kvq_fault_status(int clear) {
     const unsigned int zero = 0;
     if (cudaMemcpyToSymbol(g_kvq_fault, &zero, sizeof zero) != cudaSuccess) return -1;
   }
-  return static_cast<int>(v | kvq_attn_fault_word(clear) | kvq_ex_fault_word(clear));
+  return static_cast<int>(v | kvq_attn_fault_word(clear) | kvq_ex_fault_word(clear) |
+                          kvq_paged_fault_word(clear));
 }
 
 int kvq_selftest_wait_timeout(uint32_t limit, void* stream) {
@@ -1453,6 +1457,7 @@ const char* kvq_status_string(int status) {
     case KVQ_ERR_GROUP: return "KVQ_ERR_GROUP: group must be a power of two in [16, D]";
     case KVQ_ERR_COUNT: return "KVQ_ERR_COUNT: n_vec must be in [0, 2^31 - 256]";
     case KVQ_ERR_LAUNCH: return "KVQ_ERR_LAUNCH: the kernel launch failed";
+    case KVQ_ERR_FORMAT: return "KVQ_ERR_FORMAT: unknown block size, code format or element type";
     default: return "unknown kvq status";
   }
 }
@@ -1460,9 +1465,10 @@ const char* kvq_status_string(int status) {
 int kvq_last_cuda_error(void) {
   if (g_last_cuda_error) return g_last_cuda_error;
   if (const int e = kvq_attn_last_cuda_error()) return e;
-  return kvq_ex_last_cuda_error();
+  if (const int e = kvq_ex_last_cuda_error()) return e;
+  return kvq_paged_last_cuda_error();
 }
 
-int kvq_version(void) { return (1 << 16) | 2; }
+int kvq_version(void) { return (1 << 16) | 3; }
 
 }  // extern "C"

@@ -1,0 +1,514 @@
+// kvq_paged.cu -- the paged 8-bit cache (include/kvq.h): kvq_paged_write and
+// kvq_paged_read, and the C ABI of the attention over it.
+
+#include <cuda_runtime.h>
+
+#include <cmath>
+#include <cstdint>
+
+#include "kvq.h"
+#include "kvq_paged.cuh"
+
+namespace {
+
+using namespace kvqp;
+
+__device__ unsigned int g_paged_fault = 0;
+thread_local int g_paged_cuda_error = 0;
+
+__device__ __forceinline__ void report(unsigned bad) {
+  if (bad) atomicOr(&g_paged_fault, bad);
+}
+
+struct Tokens {
+  const int32_t* cu;      // [B + 1]
+  const int32_t* start;   // [B]
+  int64_t n_tokens;
+};
+
+// What one thread block works on: the tokens of one sequence that fall into
+// one cache block, of one KV head, in K or V.
+struct Item {
+  int id;                 // cache block, or -1: nothing to do
+  int head;
+  bool is_v;
+  int slot;               // the first token's slot
+  int count;              // tokens
+  int64_t row;            // the first token's row in the packed tensors
+};
+
+// Item numbers run over (sequence, block of its new tokens, head, K or V), the
+// last fastest: neighbouring thread blocks read neighbouring pieces of the
+// same token rows.  A sequence of n tokens touches at most floor(n / block) + 2
+// blocks.
+__device__ __forceinline__ Item find_item(const Cache& c, const Tokens& t, unsigned& bad) {
+  __shared__ Item item;
+  if (threadIdx.x < 32) {
+    const int lane = threadIdx.x;
+    int64_t x = blockIdx.x;
+    Item it;
+    it.id = -1;
+    it.is_v = x & 1;
+    x >>= 1;
+    it.head = static_cast<int>(x % c.Hkv);
+    x /= c.Hkv;
+    const int b = find_sequence(t.cu, c.B, x, 1, c.block, 2, lane);
+    const int64_t j = x - item_base(t.cu, b, 1, c.block, 2);
+    const int64_t c0 = t.cu[b], c1 = t.cu[b + 1], p0 = t.start[b];
+    if (c0 < 0 || c1 < c0 || c1 > t.n_tokens || (p0 < 0 && c1 > c0)) {
+      bad |= kFaultLength;
+    } else if (c1 > c0 && j >= 0) {
+      const int64_t blk = (p0 >> c.log_block) + j;
+      const int64_t lo = max(p0, blk << c.log_block), hi = min(p0 + (c1 - c0), (blk + 1) << c.log_block);
+      if (lo < hi) {
+        it.id = block_at(c, b, blk, bad);
+        it.slot = static_cast<int>(lo & (c.block - 1));
+        it.count = static_cast<int>(hi - lo);
+        it.row = c0 + (lo - p0);
+      }
+    }
+    if (lane == 0) {
+      item = it;
+      report(bad);
+    }
+  }
+  __syncthreads();
+  return item;
+}
+
+// ---------------------------------------------------------------------------
+// Write.  A thread block holds its tokens' channels in registers (16
+// neighbouring channels a unit, at most VPT units a thread), so the cache
+// block's largest magnitude is known before the codes are made and every input
+// is read once.  Where an older scale has to grow, the codes of the earlier
+// slots are rounded again; the arithmetic is the header's, one IEEE operation
+// at a time.
+// ---------------------------------------------------------------------------
+template <int FMT, bool BF16, int T, int VPT>
+__global__ void __launch_bounds__(T) paged_write_kernel(Cache c, Tokens t, const uint16_t* __restrict__ k,
+                                                        const uint16_t* __restrict__ v, int64_t k_stride,
+                                                        int64_t v_stride) {
+  unsigned bad = 0;
+  const Item it = find_item(c, t, bad);
+  if (it.id < 0) return;
+  const uint16_t* x = (it.is_v ? v : k) + it.row * (it.is_v ? v_stride : k_stride) + static_cast<int64_t>(it.head) * c.D;
+  const int64_t stride = it.is_v ? v_stride : k_stride;
+  const int64_t bh = static_cast<int64_t>(it.id) * c.Hkv + it.head;
+  float* scale = (it.is_v ? c.vs : c.ks) + bh;
+  uint8_t* codes = (it.is_v ? c.vc : c.kc) + bh * c.block * c.D;
+  const int upr = c.D >> 4;                       // units of a row, a power of two
+  const int lu = 31 - __clz(upr);
+  const int units = it.count << lu;
+  const float old = it.slot > 0 ? *scale : 0.0f;  // read by all before thread 0 writes it
+
+  uint4 r[VPT][2];
+  float a = 0.0f;
+#pragma unroll
+  for (int i = 0; i < VPT; ++i) {
+    const int u = threadIdx.x + i * T;
+    if (u < units) {
+      const uint4* p = reinterpret_cast<const uint4*>(x + (u >> lu) * stride + ((u & (upr - 1)) << 4));
+      r[i][0] = __ldcs(p);
+      r[i][1] = __ldcs(p + 1);
+    } else {
+      r[i][0] = r[i][1] = make_uint4(0, 0, 0, 0);
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < VPT; ++i)
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const uint32_t w[4] = {r[i][h].x, r[i][h].y, r[i][h].z, r[i][h].w};
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float2 f = unpack2<BF16>(w[e]);
+        a = fmaxf(a, fmaxf(fabsf(f.x), fabsf(f.y)));   // a NaN is passed over
+      }
+    }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) a = fmaxf(a, __shfl_xor_sync(kAll, a, o));
+  __shared__ float most[T / 32];
+  if ((threadIdx.x & 31) == 0) most[threadIdx.x >> 5] = a;
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < T / 32; ++w) a = fmaxf(a, most[w]);
+
+  constexpr float inv_q = FMT == kInt8 ? 1.0f / 127.0f : 1.0f / 448.0f;
+  const float s = fminf(fmaxf(a * inv_q, kScaleMin), kScaleMax);
+  const float S = fmaxf(old, s);                  // a NaN in the old scale is passed over
+  const float inv = __fdiv_rn(1.0f, S);
+  if (threadIdx.x == 0) *scale = S;
+
+#pragma unroll
+  for (int i = 0; i < VPT; ++i) {
+    const int u = threadIdx.x + i * T;
+    if (u < units) {
+      uint32_t q[4];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const uint32_t w[4] = {r[i][h].x, r[i][h].y, r[i][h].z, r[i][h].w};
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const float2 f = unpack2<BF16>(w[2 * e]), g = unpack2<BF16>(w[2 * e + 1]);
+          q[2 * h + e] = encode4<FMT>(f.x * inv, f.y * inv, g.x * inv, g.y * inv);
+        }
+      }
+      *reinterpret_cast<uint4*>(codes + (static_cast<int64_t>(it.slot) << lu << 4) + (static_cast<int64_t>(u) << 4)) =
+          make_uint4(q[0], q[1], q[2], q[3]);
+    }
+  }
+  if (it.slot > 0 && S > old) {
+    const float f = __fdiv_rn(old, S);
+    for (int u = threadIdx.x; u < (it.slot << lu); u += T) {
+      uint4* p = reinterpret_cast<uint4*>(codes) + u;
+      const uint4 w = *p;
+      const uint32_t in[4] = {w.x, w.y, w.z, w.w};
+      uint32_t q[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        float y[4];
+        decode4<FMT>(in[e], y);
+        q[e] = encode4<FMT>(y[0] * f, y[1] * f, y[2] * f, y[3] * f);
+      }
+      *p = make_uint4(q[0], q[1], q[2], q[3]);
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Read: the write's items, each unit of 16 codes to 32 bytes of output.
+// ---------------------------------------------------------------------------
+template <int FMT, bool BF16, int T>
+__global__ void __launch_bounds__(T) paged_read_kernel(Cache c, Tokens t, uint16_t* __restrict__ k,
+                                                       uint16_t* __restrict__ v) {
+  unsigned bad = 0;
+  const Item it = find_item(c, t, bad);
+  if (it.id < 0) return;
+  const int64_t stride = static_cast<int64_t>(c.Hkv) * c.D;
+  uint16_t* x = (it.is_v ? v : k) + it.row * stride + static_cast<int64_t>(it.head) * c.D;
+  const int64_t bh = static_cast<int64_t>(it.id) * c.Hkv + it.head;
+  const float S = (it.is_v ? c.vs : c.ks)[bh];
+  const int upr = c.D >> 4, lu = 31 - __clz(upr);
+  const uint4* codes = reinterpret_cast<const uint4*>((it.is_v ? c.vc : c.kc) + bh * c.block * c.D) + (it.slot << lu);
+  const int units = it.count << lu;
+  for (int u = threadIdx.x; u < units; u += T) {
+    const uint4 w = codes[u];
+    const uint32_t in[4] = {w.x, w.y, w.z, w.w};
+    uint32_t o[8];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      float y[4];
+      decode4<FMT>(in[e], y);
+      o[2 * e] = pack2<BF16>(y[0] * S, y[1] * S);
+      o[2 * e + 1] = pack2<BF16>(y[2] * S, y[3] * S);
+    }
+    uint4* p = reinterpret_cast<uint4*>(x + (u >> lu) * stride + ((u & (upr - 1)) << 4));
+    __stcs(p, make_uint4(o[0], o[1], o[2], o[3]));
+    __stcs(p + 1, make_uint4(o[4], o[5], o[6], o[7]));
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Attention, one warp per (query, head): the running maximum and sum of the
+// softmax and D / 32 channels of the output in each lane's registers.
+// ---------------------------------------------------------------------------
+struct Attn {
+  const uint16_t* q;
+  uint16_t* out;
+  const int32_t* cu;        // [B + 1], or null: one query per sequence
+  const int32_t* seq_len;
+  int64_t q_stride, total_q;
+  int Hq, window;
+  float scale;              // sm_scale * log2(e)
+};
+
+template <int FMT, bool BF16, int DPL>
+__global__ void __launch_bounds__(128) paged_attention_kernel(Cache c, Attn p) {
+  const int lane = threadIdx.x & 31;
+  const int64_t w = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 5);
+  if (w >= p.total_q * p.Hq) return;
+  const int64_t row = w / p.Hq;
+  const int h = static_cast<int>(w % p.Hq), kvh = h / (p.Hq / c.Hkv);
+  unsigned bad = 0;
+  int b = static_cast<int>(row);
+  int64_t L, pos;
+  const int64_t room = static_cast<int64_t>(c.max_blocks) * c.block;
+  if (p.cu) {
+    b = 0;
+    while (b < c.B && p.cu[b + 1] <= row) ++b;     // the sequence of this row
+    if (b == c.B) return;
+    L = p.seq_len[b];
+    if (L < 0 || L > room) { bad |= kFaultLength; L = L < 0 ? 0 : room; }
+    pos = L - (p.cu[b + 1] - row);
+  } else {
+    L = p.seq_len[b];
+    if (L < 0 || L > room) { bad |= kFaultLength; L = L < 0 ? 0 : room; }
+    pos = L - 1;
+  }
+  const uint16_t* q = p.q + row * p.q_stride + static_cast<int64_t>(h) * c.D + lane * DPL;
+  float x[DPL], o[DPL], m = -INFINITY, l = 0.0f;
+#pragma unroll
+  for (int i = 0; i < DPL; ++i) {
+    x[i] = BF16 ? __uint_as_float(static_cast<uint32_t>(q[i]) << 16) : __half2float(__ushort_as_half(q[i]));
+    o[i] = 0.0f;
+  }
+  const int64_t t0 = p.window > 0 ? max(int64_t{0}, pos - p.window + 1) : 0;
+  for (int64_t t = t0; t <= pos; ++t) {
+    const int id = block_at(c, b, t >> c.log_block, bad);
+    if (id < 0) continue;
+    const int64_t bh = static_cast<int64_t>(id) * c.Hkv + kvh;
+    const int64_t at = (bh * c.block + (t & (c.block - 1))) * c.D + lane * DPL;
+    float kx[DPL], vx[DPL];
+    if constexpr (DPL == 2) {
+      float f[4];
+      decode4<FMT>(*reinterpret_cast<const uint16_t*>(c.kc + at), f); kx[0] = f[0]; kx[1] = f[1];
+      decode4<FMT>(*reinterpret_cast<const uint16_t*>(c.vc + at), f); vx[0] = f[0]; vx[1] = f[1];
+    } else {
+#pragma unroll
+      for (int i = 0; i < DPL; i += 4) {
+        float f[4];
+        decode4<FMT>(*reinterpret_cast<const uint32_t*>(c.kc + at + i), f);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) kx[i + e] = f[e];
+        decode4<FMT>(*reinterpret_cast<const uint32_t*>(c.vc + at + i), f);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) vx[i + e] = f[e];
+      }
+    }
+    float s = 0.0f;
+#pragma unroll
+    for (int i = 0; i < DPL; ++i) s += x[i] * kx[i];
+#pragma unroll
+    for (int k = 16; k > 0; k >>= 1) s += __shfl_xor_sync(kAll, s, k);
+    s *= p.scale * c.ks[bh];
+    const float mn = fmaxf(m, s);
+    const float ref = mn == -INFINITY ? 0.0f : mn;             // a NaN score stays one
+    const float e0 = exp2f(m - ref), e1 = exp2f(s - ref);
+    const float pv = e1 * fmaxf(c.vs[bh], kScaleMin);
+    l = l * e0 + e1;
+#pragma unroll
+    for (int i = 0; i < DPL; ++i) o[i] = o[i] * e0 + pv * vx[i];
+    m = mn;
+  }
+  if (bad && lane == 0) report(bad);
+  const float inv = l > 0.0f || l != l ? 1.0f / l : 0.0f;
+  uint16_t* out = p.out + (row * p.Hq + h) * c.D + lane * DPL;
+#pragma unroll
+  for (int i = 0; i < DPL; i += 2) *reinterpret_cast<uint32_t*>(out + i) = pack2<BF16>(o[i] * inv, o[i + 1] * inv);
+}
+
+// ---------------------------------------------------------------------------
+// Argument checks and launches.
+// ---------------------------------------------------------------------------
+
+bool aligned_to(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
+
+int check_shape(int dtype, int format, int B, int max_blocks, int Hkv, int D, int block, int64_t num_blocks) {
+  if (D != 64 && D != 128 && D != 256) return KVQ_ERR_DIM;
+  if (block != 16 && block != 32 && block != 64 && block != 128) return KVQ_ERR_FORMAT;
+  if ((dtype != KVQ_FP16 && dtype != KVQ_BF16) || (format != KVQ_INT8 && format != KVQ_E4M3)) return KVQ_ERR_FORMAT;
+  if (B < 0 || max_blocks < 0 || Hkv < 1 || num_blocks < 0 || num_blocks > INT32_MAX) return KVQ_ERR_COUNT;
+  if (static_cast<int64_t>(max_blocks) * block > INT32_MAX) return KVQ_ERR_COUNT;
+  // both factors are below 2^31, so neither product overflows 64 bits
+  if (num_blocks * Hkv > INT32_MAX || num_blocks * Hkv * block > INT32_MAX) return KVQ_ERR_COUNT;
+  return KVQ_OK;
+}
+
+int check_stride(int64_t stride, int heads, int D) {
+  return stride % 8 == 0 && stride >= static_cast<int64_t>(heads) * D && stride <= (int64_t{1} << 40) ? KVQ_OK
+                                                                                                   : KVQ_ERR_COUNT;
+}
+
+Cache make_cache(const void* kc, const void* vc, const float* ks, const float* vs, const int32_t* table, int B,
+                 int max_blocks, int Hkv, int D, int block, int64_t num_blocks) {
+  Cache c;
+  c.kc = static_cast<uint8_t*>(const_cast<void*>(kc));
+  c.vc = static_cast<uint8_t*>(const_cast<void*>(vc));
+  c.ks = const_cast<float*>(ks);
+  c.vs = const_cast<float*>(vs);
+  c.table = table;
+  c.num_blocks = num_blocks;
+  c.B = B; c.max_blocks = max_blocks; c.Hkv = Hkv; c.D = D; c.block = block;
+  c.log_block = block == 16 ? 4 : block == 32 ? 5 : block == 64 ? 6 : 7;
+  return c;
+}
+
+int finish() {
+  const cudaError_t e = cudaGetLastError();
+  if (e == cudaSuccess) return KVQ_OK;
+  g_paged_cuda_error = static_cast<int>(e);
+  return KVQ_ERR_LAUNCH;
+}
+
+// The number of items of find_item, or 0 if there are too many for one grid.
+int64_t item_count(const Cache& c, int64_t n_tokens) {
+  const int64_t n = (n_tokens / c.block + 2 * static_cast<int64_t>(c.B)) * c.Hkv * 2;
+  return n <= INT32_MAX ? n : 0;
+}
+
+template <int FMT, bool BF16>
+void launch_write(const Cache& c, const Tokens& t, unsigned grid, const void* k, const void* v, int64_t ks, int64_t vs,
+                  cudaStream_t st) {
+  const uint16_t *kk = static_cast<const uint16_t*>(k), *vv = static_cast<const uint16_t*>(v);
+  switch (c.block * c.D >> 4) {                   // units of a full cache block
+    case 64: case 128: paged_write_kernel<FMT, BF16, 128, 1><<<grid, 128, 0, st>>>(c, t, kk, vv, ks, vs); break;
+    case 256: paged_write_kernel<FMT, BF16, 128, 2><<<grid, 128, 0, st>>>(c, t, kk, vv, ks, vs); break;
+    case 512: paged_write_kernel<FMT, BF16, 128, 4><<<grid, 128, 0, st>>>(c, t, kk, vv, ks, vs); break;
+    case 1024: paged_write_kernel<FMT, BF16, 256, 4><<<grid, 256, 0, st>>>(c, t, kk, vv, ks, vs); break;
+    default: paged_write_kernel<FMT, BF16, 256, 8><<<grid, 256, 0, st>>>(c, t, kk, vv, ks, vs); break;
+  }
+}
+
+template <int FMT, bool BF16>
+void launch_attention(const Cache& c, const Attn& p, cudaStream_t st) {
+  const unsigned grid = static_cast<unsigned>((p.total_q * p.Hq + 3) / 4);
+  switch (c.D) {
+    case 64: paged_attention_kernel<FMT, BF16, 2><<<grid, 128, 0, st>>>(c, p); break;
+    case 128: paged_attention_kernel<FMT, BF16, 4><<<grid, 128, 0, st>>>(c, p); break;
+    default: paged_attention_kernel<FMT, BF16, 8><<<grid, 128, 0, st>>>(c, p); break;
+  }
+}
+
+// One of the four instances for a format and an element type.
+#define KVQP_DISPATCH(FN, format, dtype, ...)                           \
+  do {                                                                  \
+    if ((format) == KVQ_INT8) {                                         \
+      if ((dtype) == KVQ_FP16) FN<kInt8, false>(__VA_ARGS__);           \
+      else FN<kInt8, true>(__VA_ARGS__);                                \
+    } else {                                                            \
+      if ((dtype) == KVQ_FP16) FN<kE4m3, false>(__VA_ARGS__);           \
+      else FN<kE4m3, true>(__VA_ARGS__);                                \
+    }                                                                   \
+  } while (0)
+
+template <int FMT, bool BF16>
+void launch_read(const Cache& c, const Tokens& t, unsigned grid, void* k, void* v, cudaStream_t st) {
+  paged_read_kernel<FMT, BF16, 128><<<grid, 128, 0, st>>>(c, t, static_cast<uint16_t*>(k), static_cast<uint16_t*>(v));
+}
+
+int attention(const void* q, int dtype, int64_t q_stride, const int32_t* cu_q, const int32_t* seq_len,
+              const int32_t* table, int B, int max_blocks, int64_t total_q, int Hq, int Hkv, int D, int block,
+              int format, int64_t num_blocks, const void* kc, const void* vc, const float* ks, const float* vs,
+              float sm_scale, int window, void* out, cudaStream_t st) {
+  int rc = check_shape(dtype, format, B, max_blocks, Hkv, D, block, num_blocks);
+  if (rc != KVQ_OK) return rc;
+  if (Hq < Hkv || Hq % Hkv != 0 || total_q < 0 || total_q > INT32_MAX || total_q * Hq > INT32_MAX || window < 0 ||
+      !std::isfinite(sm_scale))
+    return KVQ_ERR_COUNT;
+  rc = check_stride(q_stride, Hq, D);
+  if (rc != KVQ_OK) return rc;
+  if (B == 0 || total_q == 0) return KVQ_OK;
+  if (!q || !seq_len || !table || !kc || !vc || !ks || !vs || !out) return KVQ_ERR_NULL;
+  if (!aligned_to(q, 16) || !aligned_to(kc, 16) || !aligned_to(vc, 16) || !aligned_to(out, 16) ||
+      !aligned_to(seq_len, 4) || !aligned_to(table, 4) || !aligned_to(ks, 4) || !aligned_to(vs, 4) ||
+      !aligned_to(cu_q, 4))
+    return KVQ_ERR_ALIGN;
+  const Cache c = make_cache(kc, vc, ks, vs, table, B, max_blocks, Hkv, D, block, num_blocks);
+  Attn p;
+  p.q = static_cast<const uint16_t*>(q);
+  p.out = static_cast<uint16_t*>(out);
+  p.cu = cu_q; p.seq_len = seq_len; p.q_stride = q_stride; p.total_q = total_q; p.Hq = Hq; p.window = window;
+  p.scale = static_cast<float>(static_cast<double>(sm_scale) * 1.4426950408889634);
+  (void)cudaGetLastError();
+  KVQP_DISPATCH(launch_attention, format, dtype, c, p, st);
+  return finish();
+}
+
+}  // namespace
+
+__attribute__((visibility("hidden"))) unsigned int kvq_paged_fault_word(int clear) {
+  unsigned int v = 0;
+  if (cudaMemcpyFromSymbol(&v, g_paged_fault, sizeof(v)) != cudaSuccess) return 0;
+  if (clear && v) {
+    const unsigned int zero = 0;
+    cudaMemcpyToSymbol(g_paged_fault, &zero, sizeof(zero));
+  }
+  return v;
+}
+__attribute__((visibility("hidden"))) int kvq_paged_last_cuda_error() { return g_paged_cuda_error; }
+
+extern "C" {
+
+int kvq_paged_write(const void* k, const void* v, int dtype, int64_t k_stride, int64_t v_stride,
+                    const int32_t* cu_tokens, const int32_t* start, const int32_t* block_table, int B, int max_blocks,
+                    int64_t n_tokens, int Hkv, int D, int block, int format, int64_t num_blocks, void* k_codes,
+                    void* v_codes, float* k_scales, float* v_scales, void* stream) {
+  int rc = check_shape(dtype, format, B, max_blocks, Hkv, D, block, num_blocks);
+  if (rc != KVQ_OK) return rc;
+  if (n_tokens < 0 || n_tokens > INT32_MAX) return KVQ_ERR_COUNT;
+  if (check_stride(k_stride, Hkv, D) != KVQ_OK || check_stride(v_stride, Hkv, D) != KVQ_OK) return KVQ_ERR_COUNT;
+  if (B == 0 || n_tokens == 0) return KVQ_OK;
+  if (!k || !v || !cu_tokens || !start || !block_table || !k_codes || !v_codes || !k_scales || !v_scales)
+    return KVQ_ERR_NULL;
+  if (!aligned_to(k, 16) || !aligned_to(v, 16) || !aligned_to(k_codes, 16) || !aligned_to(v_codes, 16) ||
+      !aligned_to(cu_tokens, 4) || !aligned_to(start, 4) || !aligned_to(block_table, 4) || !aligned_to(k_scales, 4) ||
+      !aligned_to(v_scales, 4))
+    return KVQ_ERR_ALIGN;
+  const Cache c = make_cache(k_codes, v_codes, k_scales, v_scales, block_table, B, max_blocks, Hkv, D, block, num_blocks);
+  const Tokens t{cu_tokens, start, n_tokens};
+  const int64_t items = item_count(c, n_tokens);
+  if (items == 0) return KVQ_ERR_COUNT;
+  (void)cudaGetLastError();
+  KVQP_DISPATCH(launch_write, format, dtype, c, t, static_cast<unsigned>(items), k, v, k_stride, v_stride,
+                static_cast<cudaStream_t>(stream));
+  return finish();
+}
+
+int kvq_paged_read(const int32_t* cu_tokens, const int32_t* start, const int32_t* block_table, int B, int max_blocks,
+                   int64_t n_tokens, int Hkv, int D, int block, int format, int64_t num_blocks, const void* k_codes,
+                   const void* v_codes, const float* k_scales, const float* v_scales, int dtype, void* k_out,
+                   void* v_out, void* stream) {
+  int rc = check_shape(dtype, format, B, max_blocks, Hkv, D, block, num_blocks);
+  if (rc != KVQ_OK) return rc;
+  if (n_tokens < 0 || n_tokens > INT32_MAX) return KVQ_ERR_COUNT;
+  if (B == 0 || n_tokens == 0) return KVQ_OK;
+  if (!cu_tokens || !start || !block_table || !k_codes || !v_codes || !k_scales || !v_scales || !k_out || !v_out)
+    return KVQ_ERR_NULL;
+  if (!aligned_to(k_out, 16) || !aligned_to(v_out, 16) || !aligned_to(k_codes, 16) || !aligned_to(v_codes, 16) ||
+      !aligned_to(cu_tokens, 4) || !aligned_to(start, 4) || !aligned_to(block_table, 4) || !aligned_to(k_scales, 4) ||
+      !aligned_to(v_scales, 4))
+    return KVQ_ERR_ALIGN;
+  const Cache c = make_cache(k_codes, v_codes, k_scales, v_scales, block_table, B, max_blocks, Hkv, D, block, num_blocks);
+  const Tokens t{cu_tokens, start, n_tokens};
+  const int64_t items = item_count(c, n_tokens);
+  if (items == 0) return KVQ_ERR_COUNT;
+  (void)cudaGetLastError();
+  KVQP_DISPATCH(launch_read, format, dtype, c, t, static_cast<unsigned>(items), k_out, v_out,
+                static_cast<cudaStream_t>(stream));
+  return finish();
+}
+
+int64_t kvq_paged_workspace_bytes(int B, int max_blocks, int64_t total_q, int Hq, int Hkv, int D, int block) {
+  if (check_shape(KVQ_FP16, KVQ_INT8, B, max_blocks, Hkv, D, block, 0) != KVQ_OK) return -1;
+  if (Hq < Hkv || Hq % Hkv != 0 || total_q < 0 || total_q > INT32_MAX || total_q * Hq > INT32_MAX) return -1;
+  return 0;
+}
+
+int kvq_paged_attention_decode(const void* q, int dtype, int64_t q_stride, const int32_t* seq_len,
+                               const int32_t* block_table, int B, int max_blocks, int Hq, int Hkv, int D, int block,
+                               int format, int64_t num_blocks, const void* k_codes, const void* v_codes,
+                               const float* k_scales, const float* v_scales, float sm_scale, int window, void* out,
+                               void* workspace, int64_t workspace_bytes, void* stream) {
+  (void)workspace; (void)workspace_bytes;
+  return attention(q, dtype, q_stride, nullptr, seq_len, block_table, B, max_blocks, B, Hq, Hkv, D, block, format,
+                   num_blocks, k_codes, v_codes, k_scales, v_scales, sm_scale, window, out,
+                   static_cast<cudaStream_t>(stream));
+}
+
+int kvq_paged_attention_prefill(const void* q, int dtype, int64_t q_stride, const int32_t* cu_q,
+                                const int32_t* seq_len, const int32_t* block_table, int B, int max_blocks,
+                                int64_t total_q, int Hq, int Hkv, int D, int block, int format, int64_t num_blocks,
+                                const void* k_codes, const void* v_codes, const float* k_scales,
+                                const float* v_scales, float sm_scale, int window, void* out, void* workspace,
+                                int64_t workspace_bytes, void* stream) {
+  (void)workspace; (void)workspace_bytes;
+  if (!cu_q && B > 0 && total_q > 0) {
+    const int rc = check_shape(dtype, format, B, max_blocks, Hkv, D, block, num_blocks);
+    return rc != KVQ_OK ? rc : KVQ_ERR_NULL;
+  }
+  return attention(q, dtype, q_stride, cu_q, seq_len, block_table, B, max_blocks, total_q, Hq, Hkv, D, block, format,
+                   num_blocks, k_codes, v_codes, k_scales, v_scales, sm_scale, window, out,
+                   static_cast<cudaStream_t>(stream));
+}
+
+}  // extern "C"
