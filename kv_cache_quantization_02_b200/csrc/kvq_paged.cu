@@ -3,11 +3,12 @@
 
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <cmath>
 #include <cstdint>
 
 #include "kvq.h"
-#include "kvq_paged.cuh"
+#include "kvq_paged_attn.cuh"
 
 namespace {
 
@@ -212,23 +213,13 @@ __global__ void __launch_bounds__(T) paged_read_kernel(Cache c, Tokens t, uint16
 // Attention, one warp per (query, head): the running maximum and sum of the
 // softmax and D / 32 channels of the output in each lane's registers.
 // ---------------------------------------------------------------------------
-struct Attn {
-  const uint16_t* q;
-  uint16_t* out;
-  const int32_t* cu;        // [B + 1], or null: one query per sequence
-  const int32_t* seq_len;
-  int64_t q_stride, total_q;
-  int Hq, window;
-  float scale;              // sm_scale * log2(e)
-};
-
 template <int FMT, bool BF16, int DPL>
-__global__ void __launch_bounds__(128) paged_attention_kernel(Cache c, Attn p) {
-  const int lane = threadIdx.x & 31;
+__global__ void __launch_bounds__(128) paged_attention_kernel(Cache c, AttnArgs p) {
+  const int lane = threadIdx.x & 31, Hq = c.Hkv * p.R;
   const int64_t w = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 5);
-  if (w >= p.total_q * p.Hq) return;
-  const int64_t row = w / p.Hq;
-  const int h = static_cast<int>(w % p.Hq), kvh = h / (p.Hq / c.Hkv);
+  if (w >= p.total_q * Hq) return;
+  const int64_t row = w / Hq;
+  const int h = static_cast<int>(w % Hq), kvh = h / p.R;
   unsigned bad = 0;
   int b = static_cast<int>(row);
   int64_t L, pos;
@@ -280,7 +271,7 @@ __global__ void __launch_bounds__(128) paged_attention_kernel(Cache c, Attn p) {
     for (int i = 0; i < DPL; ++i) s += x[i] * kx[i];
 #pragma unroll
     for (int k = 16; k > 0; k >>= 1) s += __shfl_xor_sync(kAll, s, k);
-    s *= p.scale * c.ks[bh];
+    s *= (p.negative ? -p.scale : p.scale) * c.ks[bh];
     const float mn = fmaxf(m, s);
     const float ref = mn == -INFINITY ? 0.0f : mn;             // a NaN score stays one
     const float e0 = exp2f(m - ref), e1 = exp2f(s - ref);
@@ -292,7 +283,7 @@ __global__ void __launch_bounds__(128) paged_attention_kernel(Cache c, Attn p) {
   }
   if (bad && lane == 0) report(bad);
   const float inv = l > 0.0f || l != l ? 1.0f / l : 0.0f;
-  uint16_t* out = p.out + (row * p.Hq + h) * c.D + lane * DPL;
+  uint16_t* out = p.out + (row * Hq + h) * c.D + lane * DPL;
 #pragma unroll
   for (int i = 0; i < DPL; i += 2) *reinterpret_cast<uint32_t*>(out + i) = pack2<BF16>(o[i] * inv, o[i + 1] * inv);
 }
@@ -318,6 +309,30 @@ int check_stride(int64_t stride, int heads, int D) {
   return stride % 8 == 0 && stride >= static_cast<int64_t>(heads) * D && stride <= (int64_t{1} << 40) ? KVQ_OK
                                                                                                    : KVQ_ERR_COUNT;
 }
+
+int sm_count() {
+  static std::atomic<int> cache[64];
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 148;
+  int v = cache[dev].load(std::memory_order_relaxed);
+  if (v == 0) {
+    if (cudaDeviceGetAttribute(&v, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || v < 1) v = 148;
+    cache[dev].store(v, std::memory_order_relaxed);
+  }
+  return v;
+}
+
+// Thread blocks of a split decode call: all that the GPU holds at once, or one
+// per four tiles of 32 keys if the table has room for fewer.
+int decode_grid(int B, int max_blocks, int Hq, int Hkv, int D, int block) {
+  const int64_t items = static_cast<int64_t>(B) * Hkv * ((Hq / Hkv + 7) / 8);
+  const int64_t tiles = (static_cast<int64_t>(max_blocks) * block + 31) / 32 + 1;
+  const int64_t full = static_cast<int64_t>(sm_count()) * (D <= 128 ? 3 : 2);
+  if (items >= full) return static_cast<int>(full);
+  const int64_t most = (items * tiles + 3) / 4;
+  return static_cast<int>(most < full ? most : full);
+}
+int64_t decode_bytes(int grid, int D) { return static_cast<int64_t>(grid) * (2 * 8 * (D + 4) * 4 + 16); }
 
 Cache make_cache(const void* kc, const void* vc, const float* ks, const float* vs, const int32_t* table, int B,
                  int max_blocks, int Hkv, int D, int block, int64_t num_blocks) {
@@ -360,8 +375,8 @@ void launch_write(const Cache& c, const Tokens& t, unsigned grid, const void* k,
 }
 
 template <int FMT, bool BF16>
-void launch_attention(const Cache& c, const Attn& p, cudaStream_t st) {
-  const unsigned grid = static_cast<unsigned>((p.total_q * p.Hq + 3) / 4);
+void launch_attention(const Cache& c, const AttnArgs& p, cudaStream_t st) {
+  const unsigned grid = static_cast<unsigned>((p.total_q * c.Hkv * p.R + 3) / 4);
   switch (c.D) {
     case 64: paged_attention_kernel<FMT, BF16, 2><<<grid, 128, 0, st>>>(c, p); break;
     case 128: paged_attention_kernel<FMT, BF16, 4><<<grid, 128, 0, st>>>(c, p); break;
@@ -386,12 +401,15 @@ void launch_read(const Cache& c, const Tokens& t, unsigned grid, void* k, void* 
   paged_read_kernel<FMT, BF16, 128><<<grid, 128, 0, st>>>(c, t, static_cast<uint16_t*>(k), static_cast<uint16_t*>(v));
 }
 
-int attention(const void* q, int dtype, int64_t q_stride, const int32_t* cu_q, const int32_t* seq_len,
-              const int32_t* table, int B, int max_blocks, int64_t total_q, int Hq, int Hkv, int D, int block,
-              int format, int64_t num_blocks, const void* kc, const void* vc, const float* ks, const float* vs,
-              float sm_scale, int window, void* out, cudaStream_t st) {
+// The checks and arguments that both attentions share.  KVQ_OK with nothing to
+// do leaves p.q null.
+int attention_args(AttnArgs& p, const void* q, int dtype, int64_t q_stride, const int32_t* cu_q,
+                   const int32_t* seq_len, const int32_t* table, int B, int max_blocks, int64_t total_q, int Hq,
+                   int Hkv, int D, int block, int format, int64_t num_blocks, const void* kc, const void* vc,
+                   const float* ks, const float* vs, float sm_scale, int window, void* out) {
   int rc = check_shape(dtype, format, B, max_blocks, Hkv, D, block, num_blocks);
   if (rc != KVQ_OK) return rc;
+  p.q = nullptr;
   if (Hq < Hkv || Hq % Hkv != 0 || total_q < 0 || total_q > INT32_MAX || total_q * Hq > INT32_MAX || window < 0 ||
       !std::isfinite(sm_scale))
     return KVQ_ERR_COUNT;
@@ -403,15 +421,14 @@ int attention(const void* q, int dtype, int64_t q_stride, const int32_t* cu_q, c
       !aligned_to(seq_len, 4) || !aligned_to(table, 4) || !aligned_to(ks, 4) || !aligned_to(vs, 4) ||
       !aligned_to(cu_q, 4))
     return KVQ_ERR_ALIGN;
-  const Cache c = make_cache(kc, vc, ks, vs, table, B, max_blocks, Hkv, D, block, num_blocks);
-  Attn p;
+  p.c = make_cache(kc, vc, ks, vs, table, B, max_blocks, Hkv, D, block, num_blocks);
   p.q = static_cast<const uint16_t*>(q);
   p.out = static_cast<uint16_t*>(out);
-  p.cu = cu_q; p.seq_len = seq_len; p.q_stride = q_stride; p.total_q = total_q; p.Hq = Hq; p.window = window;
-  p.scale = static_cast<float>(static_cast<double>(sm_scale) * 1.4426950408889634);
-  (void)cudaGetLastError();
-  KVQP_DISPATCH(launch_attention, format, dtype, c, p, st);
-  return finish();
+  p.cu = cu_q; p.seq_len = seq_len; p.part = nullptr;
+  p.q_stride = q_stride; p.total_q = total_q;
+  p.R = Hq / Hkv; p.window = window; p.bf16 = dtype == KVQ_BF16; p.negative = sm_scale < 0.0f;
+  p.scale = static_cast<float>(std::fabs(static_cast<double>(sm_scale)) * 1.4426950408889634);
+  return KVQ_OK;
 }
 
 }  // namespace
@@ -423,7 +440,7 @@ __attribute__((visibility("hidden"))) unsigned int kvq_paged_fault_word(int clea
     const unsigned int zero = 0;
     cudaMemcpyToSymbol(g_paged_fault, &zero, sizeof(zero));
   }
-  return v;
+  return v | kvq_paged_decode_fault_word(clear);
 }
 __attribute__((visibility("hidden"))) int kvq_paged_last_cuda_error() { return g_paged_cuda_error; }
 
@@ -481,7 +498,7 @@ int kvq_paged_read(const int32_t* cu_tokens, const int32_t* start, const int32_t
 int64_t kvq_paged_workspace_bytes(int B, int max_blocks, int64_t total_q, int Hq, int Hkv, int D, int block) {
   if (check_shape(KVQ_FP16, KVQ_INT8, B, max_blocks, Hkv, D, block, 0) != KVQ_OK) return -1;
   if (Hq < Hkv || Hq % Hkv != 0 || total_q < 0 || total_q > INT32_MAX || total_q * Hq > INT32_MAX) return -1;
-  return 0;
+  return decode_bytes(decode_grid(B, max_blocks, Hq, Hkv, D, block), D);
 }
 
 int kvq_paged_attention_decode(const void* q, int dtype, int64_t q_stride, const int32_t* seq_len,
@@ -489,10 +506,19 @@ int kvq_paged_attention_decode(const void* q, int dtype, int64_t q_stride, const
                                int format, int64_t num_blocks, const void* k_codes, const void* v_codes,
                                const float* k_scales, const float* v_scales, float sm_scale, int window, void* out,
                                void* workspace, int64_t workspace_bytes, void* stream) {
-  (void)workspace; (void)workspace_bytes;
-  return attention(q, dtype, q_stride, nullptr, seq_len, block_table, B, max_blocks, B, Hq, Hkv, D, block, format,
-                   num_blocks, k_codes, v_codes, k_scales, v_scales, sm_scale, window, out,
-                   static_cast<cudaStream_t>(stream));
+  AttnArgs p;
+  const int rc = attention_args(p, q, dtype, q_stride, nullptr, seq_len, block_table, B, max_blocks, B, Hq, Hkv, D,
+                                block, format, num_blocks, k_codes, v_codes, k_scales, v_scales, sm_scale, window, out);
+  if (rc != KVQ_OK || p.q == nullptr) return rc;
+  const int grid = decode_grid(B, max_blocks, Hq, Hkv, D, block);
+  if (grid > 0 && workspace && aligned_to(workspace, 16) && workspace_bytes >= decode_bytes(grid, D))
+    p.part = static_cast<float*>(workspace);
+  p.blocks = grid;
+  (void)cudaGetLastError();
+  cudaError_t err = cudaSuccess;
+  if (kvq_paged_decode_launch(p, format, grid, static_cast<cudaStream_t>(stream), err) == KVQ_OK) return KVQ_OK;
+  g_paged_cuda_error = static_cast<int>(err);
+  return KVQ_ERR_LAUNCH;
 }
 
 int kvq_paged_attention_prefill(const void* q, int dtype, int64_t q_stride, const int32_t* cu_q,
@@ -502,13 +528,14 @@ int kvq_paged_attention_prefill(const void* q, int dtype, int64_t q_stride, cons
                                 const float* v_scales, float sm_scale, int window, void* out, void* workspace,
                                 int64_t workspace_bytes, void* stream) {
   (void)workspace; (void)workspace_bytes;
-  if (!cu_q && B > 0 && total_q > 0) {
-    const int rc = check_shape(dtype, format, B, max_blocks, Hkv, D, block, num_blocks);
-    return rc != KVQ_OK ? rc : KVQ_ERR_NULL;
-  }
-  return attention(q, dtype, q_stride, cu_q, seq_len, block_table, B, max_blocks, total_q, Hq, Hkv, D, block, format,
-                   num_blocks, k_codes, v_codes, k_scales, v_scales, sm_scale, window, out,
-                   static_cast<cudaStream_t>(stream));
+  AttnArgs p;
+  const int rc = attention_args(p, q, dtype, q_stride, cu_q, seq_len, block_table, B, max_blocks, total_q, Hq, Hkv, D,
+                                block, format, num_blocks, k_codes, v_codes, k_scales, v_scales, sm_scale, window, out);
+  if (rc != KVQ_OK || p.q == nullptr) return rc;
+  if (!cu_q) return KVQ_ERR_NULL;
+  (void)cudaGetLastError();
+  KVQP_DISPATCH(launch_attention, format, dtype, p.c, p, static_cast<cudaStream_t>(stream));
+  return finish();
 }
 
 }  // extern "C"

@@ -17,7 +17,6 @@ library is missing, importing this module raises ImportError.
 from __future__ import annotations
 
 import ctypes
-import functools
 import os
 
 import torch  # loads libcudart first, so the library shares torch's runtime
@@ -482,83 +481,81 @@ def dequantize(packed: torch.Tensor, scales: torch.Tensor, lam: torch.Tensor,
 
 
 # ---- the paged 8-bit cache ------------------------------------------------
+#
+# A decode step's calls are short, so these wrappers check each tensor once and
+# call the library directly.
 
 _PAGED_FORMAT = {torch.int8: KVQ_INT8, torch.float8_e4m3fn: KVQ_E4M3}
 _PAGED_DTYPE = {torch.float16: KVQ_FP16, torch.bfloat16: KVQ_BF16}
 
 
-def _paged_cache(k_cache, v_cache, k_scales, v_scales, block_table):
-    """Checks the cache and its table; (format, B, max_blocks, num_blocks, Hkv, block, D)."""
+def _paged_need(t, dtype, shape, index, name):
+    """`t` is a contiguous tensor of this type and shape on CUDA device `index`."""
+    if t.dtype is dtype and t.shape == shape and t.is_contiguous() and t.get_device() == index:
+        return
+    _need(t, dtype, shape, name)
+    raise ValueError(f"{name} must be on cuda:{index} as the other tensors, got {t.device}")
+
+
+def _paged_cache(block_table, k_cache, v_cache, k_scales, v_scales):
+    """Checks the cache and its table; (device, format, B, max_blocks, num_blocks, Hkv, block, D)."""
     if k_cache.dim() != 4 or block_table.dim() != 2:
         raise ValueError("k_cache must be [num_blocks, Hkv, block, D] and block_table [B, max_blocks]")
-    fmt = _PAGED_FORMAT.get(k_cache.dtype)
+    dtype, shape, index = k_cache.dtype, k_cache.shape, k_cache.get_device()
+    fmt = _PAGED_FORMAT.get(dtype)
     if fmt is None:
-        raise ValueError(f"k_cache must be torch.int8 or torch.float8_e4m3fn, got {k_cache.dtype}")
-    shape = k_cache.shape
+        raise ValueError(f"k_cache must be torch.int8 or torch.float8_e4m3fn, got {dtype}")
+    if index < 0:
+        raise ValueError("k_cache must be a CUDA tensor")
     num_blocks, Hkv, block, D = shape
-    _need(k_cache, k_cache.dtype, shape, "k_cache")
-    _need(v_cache, k_cache.dtype, shape, "v_cache")
-    _need(k_scales, torch.float32, (num_blocks, Hkv), "k_scales")
-    _need(v_scales, torch.float32, (num_blocks, Hkv), "v_scales")
+    _paged_need(k_cache, dtype, shape, index, "k_cache")
+    _paged_need(v_cache, dtype, shape, index, "v_cache")
+    _paged_need(k_scales, torch.float32, (num_blocks, Hkv), index, "k_scales")
+    _paged_need(v_scales, torch.float32, (num_blocks, Hkv), index, "v_scales")
     B, max_blocks = block_table.shape
-    _need(block_table, torch.int32, (B, max_blocks), "block_table")
-    return fmt, B, max_blocks, num_blocks, Hkv, block, D
+    _paged_need(block_table, torch.int32, (B, max_blocks), index, "block_table")
+    return index, fmt, B, max_blocks, num_blocks, Hkv, block, D
 
 
-def _paged_rows(x, name, D):
-    """Checks token rows [n, heads, D] that may lie apart; (element type, stride)."""
+def _paged_rows(x, name, D, index):
+    """Checks token rows [n, heads, D] that may lie apart; (element type, n, heads, stride)."""
     if x.dim() != 3 or x.shape[2] != D:
         raise ValueError(f"{name} must be [tokens, heads, {D}], got {tuple(x.shape)}")
     dtype = _PAGED_DTYPE.get(x.dtype)
     if dtype is None:
         raise ValueError(f"{name} must be torch.float16 or torch.bfloat16, got {x.dtype}")
+    if x.get_device() != index:
+        raise ValueError(f"{name} must be on cuda:{index} as the cache, got {x.device}")
     n, heads, _ = x.shape
     s0, s1, s2 = x.stride()
     if s2 != 1 or (s1 != D and heads > 1):
         raise ValueError(f"{name}: the channels and heads of a token must be contiguous")
-    return dtype, s0 if n > 1 else heads * D
+    return dtype, n, heads, s0 if n > 1 else heads * D
 
 
-def _paged_device(*tensors):
-    """The one CUDA device that all tensors are on."""
-    index = tensors[0].get_device()
-    for t in tensors:
-        if t.get_device() != index or index < 0:
-            raise ValueError("every tensor must be on the same CUDA device")
-    return index
-
-
-def _paged_call(device, fn, *args):
+def _paged_call(index, fn, *args):
     """fn(*args, stream) on the device's current stream; raises KvqError."""
-    stream = torch.cuda.current_stream(device).cuda_stream
-    if device == torch.cuda.current_device():
-        rc = fn(*args, stream)
+    if index == torch.cuda.current_device():
+        rc = fn(*args, torch.cuda.current_stream(index).cuda_stream)
     else:
-        with torch.cuda.device(device):
-            rc = fn(*args, stream)
+        with torch.cuda.device(index):
+            rc = fn(*args, torch.cuda.current_stream(index).cuda_stream)
     if rc != KVQ_OK:
         raise KvqError(rc)
 
 
-def _on_stream(fn):
-    """With `stream` given, all of the call runs under it: what it allocates
-    then belongs to that stream and is not handed out again before its work."""
-    @functools.wraps(fn)
-    def call(*args, stream=None, **kwargs):
-        if stream is None:
-            return fn(*args, **kwargs)
-        for t in (*args, *kwargs.values()):
-            if isinstance(t, torch.Tensor) and t.device != stream.device:
-                raise ValueError(f"stream is on {stream.device}, a tensor on {t.device}")
-        with torch.cuda.stream(stream):
-            return fn(*args, **kwargs)
-    return call
+def _on_stream(fn, stream, index, *args, **kwargs):
+    """A call under `stream`: what it allocates belongs to that stream, and is
+    not handed out again before its work."""
+    if stream.device.index != index:
+        raise ValueError(f"stream is on {stream.device}, the cache on cuda:{index}")
+    with torch.cuda.stream(stream):
+        return fn(*args, **kwargs)
 
 
-@_on_stream
 def paged_write(k: torch.Tensor, v: torch.Tensor, cu_tokens: torch.Tensor, start: torch.Tensor,
                 block_table: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, k_scales: torch.Tensor,
-                v_scales: torch.Tensor) -> None:
+                v_scales: torch.Tensor, stream=None) -> None:
     """Quantise new tokens into a paged 8-bit cache, in place.
 
     k, v: fp16 or bf16 [n, Hkv, D]; tokens may lie apart (slices of a fused
@@ -567,120 +564,123 @@ def paged_write(k: torch.Tensor, v: torch.Tensor, cu_tokens: torch.Tensor, start
     position p is slot p % block of block block_table[b, p // block] (int32
     [B, max_blocks]).  k_cache, v_cache: int8 or float8_e4m3fn [num_blocks,
     Hkv, block, D] with fp32 scales [num_blocks, Hkv].  This call and the three
-    below run on the current stream of the tensors' device, or, with the keyword
-    ``stream``, on that one."""
-    fmt, B, max_blocks, num_blocks, Hkv, block, D = _paged_cache(k_cache, v_cache, k_scales, v_scales, block_table)
-    n = k.shape[0]
-    dtype, k_stride = _paged_rows(k, "k", D)
-    _, v_stride = _paged_rows(v, "v", D)
-    if k.shape != (n, Hkv, D) or v.shape != (n, Hkv, D) or v.dtype != k.dtype:
+    below run on the current stream of the tensors' device, or on ``stream``."""
+    if stream is not None:
+        return _on_stream(paged_write, stream, k_cache.get_device(), k, v, cu_tokens, start, block_table, k_cache,
+                          v_cache, k_scales, v_scales)
+    index, fmt, B, max_blocks, num_blocks, Hkv, block, D = _paged_cache(block_table, k_cache, v_cache, k_scales,
+                                                                        v_scales)
+    dtype, n, heads, k_stride = _paged_rows(k, "k", D, index)
+    v_dtype, v_n, v_heads, v_stride = _paged_rows(v, "v", D, index)
+    if heads != Hkv or v_heads != Hkv or v_n != n or v_dtype != dtype:
         raise ValueError(f"k and v must both be [n, {Hkv}, {D}] of one type, "
                          f"got {tuple(k.shape)} {k.dtype} and {tuple(v.shape)} {v.dtype}")
-    _need(cu_tokens, torch.int32, (B + 1,), "cu_tokens")
-    _need(start, torch.int32, (B,), "start")
-    device = _paged_device(k, v, cu_tokens, start, block_table, k_cache, v_cache, k_scales, v_scales)
-    _paged_call(device, kvq_paged_write, k.data_ptr(), v.data_ptr(), dtype, k_stride, v_stride,
+    _paged_need(cu_tokens, torch.int32, (B + 1,), index, "cu_tokens")
+    _paged_need(start, torch.int32, (B,), index, "start")
+    _paged_call(index, _lib.kvq_paged_write, k.data_ptr(), v.data_ptr(), dtype, k_stride, v_stride,
                 cu_tokens.data_ptr(), start.data_ptr(), block_table.data_ptr(), B, max_blocks, n, Hkv, D, block, fmt,
                 num_blocks, k_cache.data_ptr(), v_cache.data_ptr(), k_scales.data_ptr(), v_scales.data_ptr())
 
 
-@_on_stream
 def paged_read(cu_tokens: torch.Tensor, start: torch.Tensor, block_table: torch.Tensor, k_cache: torch.Tensor,
                v_cache: torch.Tensor, k_scales: torch.Tensor, v_scales: torch.Tensor, n_tokens: int,
                dtype: torch.dtype = torch.float16, k_out: torch.Tensor | None = None,
-               v_out: torch.Tensor | None = None):
+               v_out: torch.Tensor | None = None, stream=None):
     """The tokens of paged_write back out of the cache -> (k, v), each
     [n_tokens, Hkv, D] of `dtype`.  Rows from cu_tokens[B] on are not written."""
-    fmt, B, max_blocks, num_blocks, Hkv, block, D = _paged_cache(k_cache, v_cache, k_scales, v_scales, block_table)
+    if stream is not None:
+        return _on_stream(paged_read, stream, k_cache.get_device(), cu_tokens, start, block_table, k_cache, v_cache,
+                          k_scales, v_scales, n_tokens, dtype, k_out, v_out)
+    index, fmt, B, max_blocks, num_blocks, Hkv, block, D = _paged_cache(block_table, k_cache, v_cache, k_scales,
+                                                                        v_scales)
     code = _PAGED_DTYPE.get(dtype)
     if code is None:
         raise ValueError(f"dtype must be torch.float16 or torch.bfloat16, got {dtype}")
-    _need(cu_tokens, torch.int32, (B + 1,), "cu_tokens")
-    _need(start, torch.int32, (B,), "start")
+    _paged_need(cu_tokens, torch.int32, (B + 1,), index, "cu_tokens")
+    _paged_need(start, torch.int32, (B,), index, "start")
     shape = (n_tokens, Hkv, D)
     if k_out is None:
         k_out = torch.empty(shape, dtype=dtype, device=k_cache.device)
+    else:
+        _paged_need(k_out, dtype, shape, index, "k_out")
     if v_out is None:
         v_out = torch.empty(shape, dtype=dtype, device=k_cache.device)
-    _need(k_out, dtype, shape, "k_out")
-    _need(v_out, dtype, shape, "v_out")
-    device = _paged_device(cu_tokens, start, block_table, k_cache, v_cache, k_scales, v_scales, k_out, v_out)
-    _paged_call(device, kvq_paged_read, cu_tokens.data_ptr(), start.data_ptr(), block_table.data_ptr(), B,
+    else:
+        _paged_need(v_out, dtype, shape, index, "v_out")
+    _paged_call(index, _lib.kvq_paged_read, cu_tokens.data_ptr(), start.data_ptr(), block_table.data_ptr(), B,
                 max_blocks, n_tokens, Hkv, D, block, fmt, num_blocks, k_cache.data_ptr(), v_cache.data_ptr(),
                 k_scales.data_ptr(), v_scales.data_ptr(), code, k_out.data_ptr(), v_out.data_ptr())
     return k_out, v_out
 
 
-def _paged_out(q, out):
-    if out is None:
-        return torch.empty(q.shape, dtype=q.dtype, device=q.device)
-    _need(out, q.dtype, q.shape, "out")
-    return out
-
-
-def _paged_workspace(workspace, device, *shape):
+def _paged_workspace(workspace, like, index, *shape):
     """(tensor or None, address, bytes): `workspace` True allocates what the library asks for."""
     if workspace is True:
-        need = kvq_paged_workspace_bytes(*shape)
+        need = _lib.kvq_paged_workspace_bytes(*shape)
         if need <= 0:
             return None, 0, 0
-        workspace = torch.empty(need, dtype=torch.uint8, device=device)
-    elif not isinstance(workspace, torch.Tensor):
+        workspace = like.new_empty(need, dtype=torch.uint8)
+        return workspace, workspace.data_ptr(), need
+    if not isinstance(workspace, torch.Tensor):
         return None, 0, 0
-    elif not workspace.is_cuda or workspace.dtype != torch.uint8 or not workspace.is_contiguous():
-        raise ValueError("workspace must be a contiguous uint8 CUDA tensor")
+    _paged_need(workspace, torch.uint8, (workspace.numel(),), index, "workspace")
     return workspace, workspace.data_ptr(), workspace.numel()
 
 
-@_on_stream
 def paged_attention_decode(q: torch.Tensor, seq_len: torch.Tensor, block_table: torch.Tensor, k_cache: torch.Tensor,
                            v_cache: torch.Tensor, k_scales: torch.Tensor, v_scales: torch.Tensor, sm_scale: float,
                            window: int = 0, out: torch.Tensor | None = None,
-                           workspace: torch.Tensor | bool = True) -> torch.Tensor:
+                           workspace: torch.Tensor | bool = True, stream=None) -> torch.Tensor:
     """Attention of one token per sequence over a paged 8-bit cache.  q fp16 or
     bf16 [B, Hq, D] (sequences may lie apart); seq_len int32 [B], the positions
     in the cache, the query's own among them; window > 0 keeps the last
     `window` of them -> [B, Hq, D].  ``workspace``: a uint8 CUDA tensor, True
     to allocate the size the library asks for, or False to run unsplit."""
-    fmt, B, max_blocks, num_blocks, Hkv, block, D = _paged_cache(k_cache, v_cache, k_scales, v_scales, block_table)
-    dtype, q_stride = _paged_rows(q, "q", D)
-    Hq = q.shape[1]
-    if q.shape[0] != B:
-        raise ValueError(f"q must have one row for each of the {B} sequences, got {q.shape[0]}")
-    _need(seq_len, torch.int32, (B,), "seq_len")
-    out = _paged_out(q, out)
-    tensors = [q, seq_len, block_table, k_cache, v_cache, k_scales, v_scales, out]
-    ws, ws_ptr, ws_bytes = _paged_workspace(workspace, q.device, B, max_blocks, B, Hq, Hkv, D, block)
-    if ws is not None:
-        tensors.append(ws)
-    _paged_call(_paged_device(*tensors), kvq_paged_attention_decode, q.data_ptr(), dtype, q_stride,
-                seq_len.data_ptr(), block_table.data_ptr(), B, max_blocks, Hq, Hkv, D, block, fmt, num_blocks,
-                k_cache.data_ptr(), v_cache.data_ptr(), k_scales.data_ptr(), v_scales.data_ptr(), float(sm_scale),
-                int(window), out.data_ptr(), ws_ptr, ws_bytes)
+    if stream is not None:
+        return _on_stream(paged_attention_decode, stream, k_cache.get_device(), q, seq_len, block_table, k_cache,
+                          v_cache, k_scales, v_scales, sm_scale, window, out, workspace)
+    index, fmt, B, max_blocks, num_blocks, Hkv, block, D = _paged_cache(block_table, k_cache, v_cache, k_scales,
+                                                                        v_scales)
+    dtype, n, Hq, q_stride = _paged_rows(q, "q", D, index)
+    if n != B:
+        raise ValueError(f"q must have one row for each of the {B} sequences, got {n}")
+    _paged_need(seq_len, torch.int32, (B,), index, "seq_len")
+    if out is None:
+        out = q.new_empty((B, Hq, D))
+    else:
+        _paged_need(out, q.dtype, (B, Hq, D), index, "out")
+    ws, ws_ptr, ws_bytes = _paged_workspace(workspace, q, index, B, max_blocks, B, Hq, Hkv, D, block)
+    _paged_call(index, _lib.kvq_paged_attention_decode, q.data_ptr(), dtype, q_stride, seq_len.data_ptr(),
+                block_table.data_ptr(), B, max_blocks, Hq, Hkv, D, block, fmt, num_blocks, k_cache.data_ptr(),
+                v_cache.data_ptr(), k_scales.data_ptr(), v_scales.data_ptr(), sm_scale, window, out.data_ptr(), ws_ptr,
+                ws_bytes)
     return out
 
 
-@_on_stream
 def paged_attention_prefill(q: torch.Tensor, cu_q: torch.Tensor, seq_len: torch.Tensor, block_table: torch.Tensor,
                             k_cache: torch.Tensor, v_cache: torch.Tensor, k_scales: torch.Tensor,
                             v_scales: torch.Tensor, sm_scale: float, window: int = 0,
-                            out: torch.Tensor | None = None, workspace: torch.Tensor | bool = True) -> torch.Tensor:
+                            out: torch.Tensor | None = None, workspace: torch.Tensor | bool = True,
+                            stream=None) -> torch.Tensor:
     """Causal attention of any number of new tokens per sequence.  q fp16 or
     bf16 [n, Hq, D], sequence b's in rows cu_q[b] .. cu_q[b + 1] (int32
     [B + 1]), the last of them at position seq_len[b] - 1; the rest as for
     paged_attention_decode -> [n, Hq, D]."""
-    fmt, B, max_blocks, num_blocks, Hkv, block, D = _paged_cache(k_cache, v_cache, k_scales, v_scales, block_table)
-    dtype, q_stride = _paged_rows(q, "q", D)
-    n, Hq, _ = q.shape
-    _need(cu_q, torch.int32, (B + 1,), "cu_q")
-    _need(seq_len, torch.int32, (B,), "seq_len")
-    out = _paged_out(q, out)
-    tensors = [q, cu_q, seq_len, block_table, k_cache, v_cache, k_scales, v_scales, out]
-    ws, ws_ptr, ws_bytes = _paged_workspace(workspace, q.device, B, max_blocks, n, Hq, Hkv, D, block)
-    if ws is not None:
-        tensors.append(ws)
-    _paged_call(_paged_device(*tensors), kvq_paged_attention_prefill, q.data_ptr(), dtype, q_stride,
-                cu_q.data_ptr(), seq_len.data_ptr(), block_table.data_ptr(), B, max_blocks, n, Hq, Hkv, D, block, fmt,
-                num_blocks, k_cache.data_ptr(), v_cache.data_ptr(), k_scales.data_ptr(), v_scales.data_ptr(),
-                float(sm_scale), int(window), out.data_ptr(), ws_ptr, ws_bytes)
+    if stream is not None:
+        return _on_stream(paged_attention_prefill, stream, k_cache.get_device(), q, cu_q, seq_len, block_table,
+                          k_cache, v_cache, k_scales, v_scales, sm_scale, window, out, workspace)
+    index, fmt, B, max_blocks, num_blocks, Hkv, block, D = _paged_cache(block_table, k_cache, v_cache, k_scales,
+                                                                        v_scales)
+    dtype, n, Hq, q_stride = _paged_rows(q, "q", D, index)
+    _paged_need(cu_q, torch.int32, (B + 1,), index, "cu_q")
+    _paged_need(seq_len, torch.int32, (B,), index, "seq_len")
+    if out is None:
+        out = q.new_empty((n, Hq, D))
+    else:
+        _paged_need(out, q.dtype, (n, Hq, D), index, "out")
+    ws, ws_ptr, ws_bytes = _paged_workspace(workspace, q, index, B, max_blocks, n, Hq, Hkv, D, block)
+    _paged_call(index, _lib.kvq_paged_attention_prefill, q.data_ptr(), dtype, q_stride, cu_q.data_ptr(),
+                seq_len.data_ptr(), block_table.data_ptr(), B, max_blocks, n, Hq, Hkv, D, block, fmt, num_blocks,
+                k_cache.data_ptr(), v_cache.data_ptr(), k_scales.data_ptr(), v_scales.data_ptr(), sm_scale, window,
+                out.data_ptr(), ws_ptr, ws_bytes)
     return out

@@ -123,8 +123,9 @@ class Case:
         The kernels hold scores and sums in fp32 (u = 2^-24) and round each softmax weight to fp16 before the
         value product.  With z the largest sum_d |q_d k_d| sm_scale over the keys, a score is off by at most
         e = (D + 8) u z (D products added in any order, the scales and the exponent's argument), plus a few u
-        of the argument itself, |s| <= z; the exponential adds 2^-21.  So each weight is off by
-        r = 2 e + 2^-21 relative (numerator and denominator), then by 2^-11 from fp16 or, below fp16's normal
+        of the argument itself, |s| <= z; the value scale's logarithm b (|b| <= y) joins the argument,
+        four roundings of it and a reference at most y + z away; the exponential adds 2^-21.  So each weight is off
+        by r = 2 e + 2^-21 + 8 u (z + y) relative (numerator and denominator), then by 2^-11 from fp16 or, below fp16's normal
         range, by 2^-25 of the largest weight times value scale of the row, which is at least 1 as the kernels
         hold it: 2^-25 Q for each of the L keys.  L additions in fp32 add (L + 64) 2 u.  With A = sum_t p_t |v_t|
         for the output's channel:
@@ -155,7 +156,8 @@ class Case:
             z = big.masked_fill(hide, 0.0).amax(-1)
             o = torch.einsum("nhrt,thd->nhrd", p, v)
             A = torch.einsum("nhrt,thd->nhrd", p, v.abs())
-            r = 2 * (D + 8) * u * z + 8 * u * z + 2.0 ** -21
+            y = sv.log2().abs().max()
+            r = 2 * (D + 8) * u * z + 8 * u * (z + y) + 2.0 ** -21
             top = (p * sv.t()[None, :, None, :]).amax(-1)
             e = o.abs() * (eps / 2 * (1 + 2.0 ** -8)) + A * (2.0 ** -11 + r + (L + 64) * 2 * u)[..., None]
             e = e + (L * 2.0 ** -25 * QMAX[self.fmt] * top)[..., None] + least
