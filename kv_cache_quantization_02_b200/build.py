@@ -17,14 +17,15 @@ ROOT = os.path.dirname(PKG)
 SOURCES = [os.path.join(PKG, "csrc", n) for n in ("kvq.cu", "kvq_attn.cu", "kvq_attn_d64.cu", "kvq_attn_d128.cu",
                                                         "kvq_attn_d256.cu", "kvq_ex.cu", "kvq_srft_d64.cu",
                                                         "kvq_srft_d96.cu", "kvq_srft_d128.cu", "kvq_srft_d256.cu",
-                                                        "kvq_paged.cu", "kvq_paged_decode.cu")]
+                                                        "kvq_paged.cu", "kvq_paged_decode.cu",
+                                                        "kvq_paged_prefill.cu")]
 # Per-unit flags.  The codec units keep --fmad=false: their results are
 # defined bit for bit, and a contracted multiply-add rounds once where the
 # codec's definition rounds twice.  The decode attention is checked against
 # the oracle to a derived tolerance, not bit for bit, so its multiply-add
 # pairs may contract (one rounding instead of two only shrinks the error).
 UNIT_FLAGS = {n: ["--fmad=true"] for n in ("kvq_attn_d64.cu", "kvq_attn_d128.cu", "kvq_attn_d256.cu",
-                                           "kvq_paged_decode.cu")}
+                                           "kvq_paged_decode.cu", "kvq_paged_prefill.cu")}
 INCLUDE = os.path.join(ROOT, "include")
 LIBRARY = os.path.join(PKG, "libkvq.so")
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")

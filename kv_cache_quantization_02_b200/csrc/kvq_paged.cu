@@ -210,85 +210,6 @@ __global__ void __launch_bounds__(T) paged_read_kernel(Cache c, Tokens t, uint16
 }
 
 // ---------------------------------------------------------------------------
-// Attention, one warp per (query, head): the running maximum and sum of the
-// softmax and D / 32 channels of the output in each lane's registers.
-// ---------------------------------------------------------------------------
-template <int FMT, bool BF16, int DPL>
-__global__ void __launch_bounds__(128) paged_attention_kernel(Cache c, AttnArgs p) {
-  const int lane = threadIdx.x & 31, Hq = c.Hkv * p.R;
-  const int64_t w = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 5);
-  if (w >= p.total_q * Hq) return;
-  const int64_t row = w / Hq;
-  const int h = static_cast<int>(w % Hq), kvh = h / p.R;
-  unsigned bad = 0;
-  int b = static_cast<int>(row);
-  int64_t L, pos;
-  const int64_t room = static_cast<int64_t>(c.max_blocks) * c.block;
-  if (p.cu) {
-    b = 0;
-    while (b < c.B && p.cu[b + 1] <= row) ++b;     // the sequence of this row
-    if (b == c.B) return;
-    L = p.seq_len[b];
-    if (L < 0 || L > room) { bad |= kFaultLength; L = L < 0 ? 0 : room; }
-    pos = L - (p.cu[b + 1] - row);
-  } else {
-    L = p.seq_len[b];
-    if (L < 0 || L > room) { bad |= kFaultLength; L = L < 0 ? 0 : room; }
-    pos = L - 1;
-  }
-  const uint16_t* q = p.q + row * p.q_stride + static_cast<int64_t>(h) * c.D + lane * DPL;
-  float x[DPL], o[DPL], m = -INFINITY, l = 0.0f;
-#pragma unroll
-  for (int i = 0; i < DPL; ++i) {
-    x[i] = BF16 ? __uint_as_float(static_cast<uint32_t>(q[i]) << 16) : __half2float(__ushort_as_half(q[i]));
-    o[i] = 0.0f;
-  }
-  const int64_t t0 = p.window > 0 ? max(int64_t{0}, pos - p.window + 1) : 0;
-  for (int64_t t = t0; t <= pos; ++t) {
-    const int id = block_at(c, b, t >> c.log_block, bad);
-    if (id < 0) continue;
-    const int64_t bh = static_cast<int64_t>(id) * c.Hkv + kvh;
-    const int64_t at = (bh * c.block + (t & (c.block - 1))) * c.D + lane * DPL;
-    float kx[DPL], vx[DPL];
-    if constexpr (DPL == 2) {
-      float f[4];
-      decode4<FMT>(*reinterpret_cast<const uint16_t*>(c.kc + at), f); kx[0] = f[0]; kx[1] = f[1];
-      decode4<FMT>(*reinterpret_cast<const uint16_t*>(c.vc + at), f); vx[0] = f[0]; vx[1] = f[1];
-    } else {
-#pragma unroll
-      for (int i = 0; i < DPL; i += 4) {
-        float f[4];
-        decode4<FMT>(*reinterpret_cast<const uint32_t*>(c.kc + at + i), f);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) kx[i + e] = f[e];
-        decode4<FMT>(*reinterpret_cast<const uint32_t*>(c.vc + at + i), f);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) vx[i + e] = f[e];
-      }
-    }
-    float s = 0.0f;
-#pragma unroll
-    for (int i = 0; i < DPL; ++i) s += x[i] * kx[i];
-#pragma unroll
-    for (int k = 16; k > 0; k >>= 1) s += __shfl_xor_sync(kAll, s, k);
-    s *= (p.negative ? -p.scale : p.scale) * c.ks[bh];
-    const float mn = fmaxf(m, s);
-    const float ref = mn == -INFINITY ? 0.0f : mn;             // a NaN score stays one
-    const float e0 = exp2f(m - ref), e1 = exp2f(s - ref);
-    const float pv = e1 * fmaxf(c.vs[bh], kScaleMin);
-    l = l * e0 + e1;
-#pragma unroll
-    for (int i = 0; i < DPL; ++i) o[i] = o[i] * e0 + pv * vx[i];
-    m = mn;
-  }
-  if (bad && lane == 0) report(bad);
-  const float inv = l > 0.0f || l != l ? 1.0f / l : 0.0f;
-  uint16_t* out = p.out + (row * Hq + h) * c.D + lane * DPL;
-#pragma unroll
-  for (int i = 0; i < DPL; i += 2) *reinterpret_cast<uint32_t*>(out + i) = pack2<BF16>(o[i] * inv, o[i + 1] * inv);
-}
-
-// ---------------------------------------------------------------------------
 // Argument checks and launches.
 // ---------------------------------------------------------------------------
 
@@ -334,6 +255,26 @@ int decode_grid(int B, int max_blocks, int Hq, int Hkv, int D, int block) {
 }
 int64_t decode_bytes(int grid, int D) { return static_cast<int64_t>(grid) * (2 * 8 * (D + 4) * 4 + 16); }
 
+// Tiles of a prompt call, and the splits of their keys: where the tiles leave
+// SMs idle, as many as fill them, each with at least two tiles of keys.
+struct PromptGrid {
+  int64_t tiles;
+  int nsplit;
+  int64_t bytes;
+};
+PromptGrid prompt_grid(int B, int max_blocks, int64_t total_q, int Hq, int Hkv, int D, int block) {
+  const int rows = D == 256 ? 128 : 256, kt = D == 256 ? 64 : 128;
+  PromptGrid g;
+  g.tiles = (total_q * (Hq / Hkv) / rows + B) * Hkv;
+  const int64_t most = static_cast<int64_t>(max_blocks) * block / kt / 2;
+  int64_t n = g.tiles > 0 ? sm_count() / g.tiles : 1;
+  n = n > most ? most : n;
+  n = n > 32 ? 32 : n;
+  g.nsplit = n > 1 ? static_cast<int>(n) : 1;
+  g.bytes = g.nsplit > 1 ? g.tiles * g.nsplit * rows * (D + 4) * 4 : 0;
+  return g;
+}
+
 Cache make_cache(const void* kc, const void* vc, const float* ks, const float* vs, const int32_t* table, int B,
                  int max_blocks, int Hkv, int D, int block, int64_t num_blocks) {
   Cache c;
@@ -371,16 +312,6 @@ void launch_write(const Cache& c, const Tokens& t, unsigned grid, const void* k,
     case 512: paged_write_kernel<FMT, BF16, 128, 4><<<grid, 128, 0, st>>>(c, t, kk, vv, ks, vs); break;
     case 1024: paged_write_kernel<FMT, BF16, 256, 4><<<grid, 256, 0, st>>>(c, t, kk, vv, ks, vs); break;
     default: paged_write_kernel<FMT, BF16, 256, 8><<<grid, 256, 0, st>>>(c, t, kk, vv, ks, vs); break;
-  }
-}
-
-template <int FMT, bool BF16>
-void launch_attention(const Cache& c, const AttnArgs& p, cudaStream_t st) {
-  const unsigned grid = static_cast<unsigned>((p.total_q * c.Hkv * p.R + 3) / 4);
-  switch (c.D) {
-    case 64: paged_attention_kernel<FMT, BF16, 2><<<grid, 128, 0, st>>>(c, p); break;
-    case 128: paged_attention_kernel<FMT, BF16, 4><<<grid, 128, 0, st>>>(c, p); break;
-    default: paged_attention_kernel<FMT, BF16, 8><<<grid, 128, 0, st>>>(c, p); break;
   }
 }
 
@@ -440,7 +371,7 @@ __attribute__((visibility("hidden"))) unsigned int kvq_paged_fault_word(int clea
     const unsigned int zero = 0;
     cudaMemcpyToSymbol(g_paged_fault, &zero, sizeof(zero));
   }
-  return v | kvq_paged_decode_fault_word(clear);
+  return v | kvq_paged_decode_fault_word(clear) | kvq_paged_prefill_fault_word(clear);
 }
 __attribute__((visibility("hidden"))) int kvq_paged_last_cuda_error() { return g_paged_cuda_error; }
 
@@ -498,7 +429,9 @@ int kvq_paged_read(const int32_t* cu_tokens, const int32_t* start, const int32_t
 int64_t kvq_paged_workspace_bytes(int B, int max_blocks, int64_t total_q, int Hq, int Hkv, int D, int block) {
   if (check_shape(KVQ_FP16, KVQ_INT8, B, max_blocks, Hkv, D, block, 0) != KVQ_OK) return -1;
   if (Hq < Hkv || Hq % Hkv != 0 || total_q < 0 || total_q > INT32_MAX || total_q * Hq > INT32_MAX) return -1;
-  return decode_bytes(decode_grid(B, max_blocks, Hq, Hkv, D, block), D);
+  const int64_t one = decode_bytes(decode_grid(B, max_blocks, Hq, Hkv, D, block), D);
+  const int64_t many = prompt_grid(B, max_blocks, total_q, Hq, Hkv, D, block).bytes;
+  return one > many ? one : many;
 }
 
 int kvq_paged_attention_decode(const void* q, int dtype, int64_t q_stride, const int32_t* seq_len,
@@ -527,15 +460,22 @@ int kvq_paged_attention_prefill(const void* q, int dtype, int64_t q_stride, cons
                                 const void* k_codes, const void* v_codes, const float* k_scales,
                                 const float* v_scales, float sm_scale, int window, void* out, void* workspace,
                                 int64_t workspace_bytes, void* stream) {
-  (void)workspace; (void)workspace_bytes;
   AttnArgs p;
   const int rc = attention_args(p, q, dtype, q_stride, cu_q, seq_len, block_table, B, max_blocks, total_q, Hq, Hkv, D,
                                 block, format, num_blocks, k_codes, v_codes, k_scales, v_scales, sm_scale, window, out);
   if (rc != KVQ_OK || p.q == nullptr) return rc;
   if (!cu_q) return KVQ_ERR_NULL;
+  PromptGrid g = prompt_grid(B, max_blocks, total_q, Hq, Hkv, D, block);
+  if (g.tiles * (D == 256 ? 16 : 32) > INT32_MAX) return KVQ_ERR_COUNT;
+  if (g.nsplit > 1 && workspace && aligned_to(workspace, 16) && workspace_bytes >= g.bytes)
+    p.part = static_cast<float*>(workspace);
+  else
+    g.nsplit = 1;
   (void)cudaGetLastError();
-  KVQP_DISPATCH(launch_attention, format, dtype, p.c, p, static_cast<cudaStream_t>(stream));
-  return finish();
+  cudaError_t err = cudaSuccess;
+  if (kvq_paged_prefill_launch(p, format, g.nsplit, static_cast<cudaStream_t>(stream), err) == KVQ_OK) return KVQ_OK;
+  g_paged_cuda_error = static_cast<int>(err);
+  return KVQ_ERR_LAUNCH;
 }
 
 }  // extern "C"

@@ -1,0 +1,677 @@
+// kvq_paged_prefill.cu -- causal attention of any number of new tokens per
+// sequence over the paged 8-bit cache (include/kvq.h,
+// kvq_paged_attention_prefill); the softmax's form is in kvq_paged_attn.cuh.
+//
+// Bound: tensor-core rate for long chunks (4 D flops a visible pair and query
+// head), the codes' bytes for a few queries over a long cache.
+//
+// Work.  The query heads of a KV head share its keys, so the rows of a tile
+// are (token, head) pairs of one KV head, R rows a token, packed across token
+// boundaries: 2 x 128 rows a thread block (128 at D = 256).  Where the tiles do
+// not fill the GPU the keys of a tile are split over several thread blocks,
+// whose partial sums a second kernel joins.
+//
+// A thread block is 16 warps in roles, coupled by mbarriers:
+//   0-7    softmax: a thread per row reads its scores from tensor memory,
+//          makes the weights and writes them back as fp16 (warps 0-3 the first
+//          128 rows, 4-7 the second; at D = 256 only 0-3);
+//   8-11   K: codes from the cache to fp16 in shared memory, 128-byte swizzled;
+//   13-15  V: the same;
+//   12     one thread issues the MMAs (tcgen05, fp16 with fp32 sums in tensor
+//          memory): S = Q K^T from shared memory, O += P V with P from tensor
+//          memory, in an order that gives the tensor cores one tile's products
+//          while the softmax works on the other's (at D = 256: the next keys'
+//          scores while it works on these).
+// Codes are exact in fp16, so K and V are converted once per thread block and
+// tile; their scales are in the softmax's exponent.  Code pairs unpack as
+// channels (0, 2), (1, 3): Q's channels are laid out in that order too, and the
+// outputs' are put back in the last step.
+// The reference of a row's softmax moves rarely (kLazy), and only then is O
+// rescaled in tensor memory, by the thread that owns the row.
+
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include <atomic>
+#include <cstdint>
+
+#include "kvq.h"
+#include "kvq_paged_attn.cuh"
+
+namespace {
+
+using namespace kvqp;
+
+#include "kvq_async.cuh"
+
+__device__ unsigned int g_prefill_fault = 0;
+
+constexpr uint32_t kSpin = 1u << 22;              // bounded mbarrier waits
+constexpr int kThreads = 512;
+constexpr int kFirstK = 8, kIssuer = 12, kFirstV = 13;     // warps
+
+template <int D>
+struct Prefill {
+  static constexpr int MT = D == 256 ? 1 : 2;     // 128-row tiles
+  static constexpr int SB = D == 256 ? 2 : 1;     // score buffers of one of them
+  static constexpr int KT = D == 256 ? 64 : 128;  // keys of a tile
+  static constexpr int ROWS = MT * 128;
+  static constexpr int CB = D / 64;               // 64-channel blocks (128-byte swizzled rows)
+  static constexpr int NSUB = KT / 16;            // 16-key parts, each inside one cache block
+  static constexpr int QBYTES = ROWS * D * 2;
+  static constexpr int TILE = KT * D * 2;         // fp16 bytes of a K or V tile
+  static constexpr int STAGES = 2;
+  static constexpr int META = 4 * NSUB * 16;      // scales of four tiles
+  static constexpr int NBAR = 4 * STAGES + 4 + 2 * 2 + 2;
+  static constexpr int SMEM = 1024 + QBYTES + 2 * STAGES * TILE + META + ROWS * 4 + NBAR * 8 + 64;
+  // tensor memory columns: scores (and weights over them), then outputs
+  static constexpr int S0 = 0, SCOLS = KT, O0 = 2 * SCOLS;
+  static constexpr uint32_t COLS = 512;
+};
+
+// ---- tcgen05 ------------------------------------------------------------------------
+
+__device__ __forceinline__ void tmem_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tmem_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// 32 columns of this thread's lane.
+__device__ __forceinline__ void tmem_ld32(uint32_t (&r)[32], uint32_t addr) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+        "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+        "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(addr));
+}
+__device__ __forceinline__ void tmem_st32(uint32_t addr, const uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31};"
+      :: "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
+         "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]),
+         "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]),
+         "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31]), "r"(addr)
+      : "memory");
+}
+
+// Shared-memory matrix descriptor with the 128-byte swizzle: start address,
+// leading and stride byte offsets in units of 16, descriptor version 1.
+__device__ __forceinline__ uint64_t matrix_desc(uint32_t addr, uint32_t leading, uint32_t stride) {
+  return static_cast<uint64_t>((addr & 0x3FFFFu) >> 4) | (static_cast<uint64_t>(leading >> 4) << 16) |
+         (static_cast<uint64_t>(stride >> 4) << 32) | (uint64_t{1} << 46) | (uint64_t{2} << 61);
+}
+// Instruction descriptor: fp16 operands, fp32 sums, M = 128.
+template <int N, bool B_TRANSPOSED>
+constexpr uint32_t kMmaDesc = (1u << 4) | (B_TRANSPOSED ? 1u << 16 : 0u) | (static_cast<uint32_t>(N >> 3) << 17) |
+                              ((128u >> 4) << 24);
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t desc, bool add) {
+  asm volatile("{\n.reg .pred p;\nsetp.ne.b32 p, %4, 0;\n"
+               "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}"
+               :: "r"(d), "l"(a), "l"(b), "r"(desc), "r"(static_cast<uint32_t>(add)) : "memory");
+}
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t desc, bool add) {
+  asm volatile("{\n.reg .pred p;\nsetp.ne.b32 p, %4, 0;\n"
+               "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}"
+               :: "r"(d), "r"(a), "l"(b), "r"(desc), "r"(static_cast<uint32_t>(add)) : "memory");
+}
+// The barrier completes when this thread's MMAs so far have.
+__device__ __forceinline__ void mma_commit(uint64_t* bar) {
+  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];"
+               :: "r"(smem_addr(bar)) : "memory");
+}
+
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+
+// What a thread block works on: rows row0 .. row0 + count - 1 of the sequence's
+// n R (token, head) pairs, against the key tiles first + KT i, i < tiles.
+struct Job {
+  int b, kvh, n, L;
+  int row0, count, q0;        // q0: the sequence's first row in the packed queries
+  int lo, hi;                 // keys that some row sees
+  int first, tiles;           // first key of the first tile; tiles of this split
+  int split;
+  int64_t tile;               // the tile's number, for partial sums
+};
+
+template <int D>
+__device__ __forceinline__ bool find_job(const AttnArgs& a, int nsplit, Job& j, unsigned& bad) {
+  using C = Prefill<D>;
+  int64_t x = blockIdx.x;
+  j.split = static_cast<int>(x % nsplit);
+  x /= nsplit;
+  j.tile = x;
+  j.kvh = static_cast<int>(x % a.c.Hkv);
+  // the last tiles of a sequence see most keys: they start first
+  const int64_t items = a.total_q * a.R / C::ROWS + a.c.B;
+  const int64_t item = items - 1 - x / a.c.Hkv;
+  j.b = find_sequence(a.cu, a.c.B, item, a.R, C::ROWS, 1, threadIdx.x & 31);
+  const int64_t k = item - item_base(a.cu, j.b, a.R, C::ROWS, 1);
+  const int64_t c0 = a.cu[j.b], c1 = a.cu[j.b + 1];
+  if (c0 < 0 || c1 < c0 || c1 > a.total_q) {
+    bad |= kFaultLength;
+    return false;
+  }
+  j.n = static_cast<int>(c1 - c0);
+  j.q0 = static_cast<int>(c0);
+  const int64_t rows = (c1 - c0) * a.R;
+  if (k < 0 || k * C::ROWS >= rows) return false;
+  j.row0 = static_cast<int>(k * C::ROWS);
+  j.count = static_cast<int>(min(static_cast<int64_t>(C::ROWS), rows - j.row0));
+  j.L = sequence_length(a, j.b, bad);
+  const int p0 = j.L - j.n + j.row0 / a.R, p1 = j.L - j.n + (j.row0 + j.count - 1) / a.R;
+  j.lo = a.window > 0 ? max(0, p0 - a.window + 1) : 0;
+  j.hi = max(0, p1 + 1);
+  j.first = j.lo / C::KT * C::KT;
+  const int tiles = j.hi > j.lo ? (j.hi - j.first + C::KT - 1) / C::KT : 0;
+  const int t0 = static_cast<int>(static_cast<int64_t>(tiles) * j.split / nsplit);
+  const int t1 = static_cast<int>(static_cast<int64_t>(tiles) * (j.split + 1) / nsplit);
+  j.first += t0 * C::KT;
+  j.tiles = t1 - t0;
+  return true;
+}
+
+// The rows in the cache of a tile's 16-key parts: lane i < NSUB gets part i's
+// first row ((block id, head, slot) as one number), or -1.
+template <int D>
+__device__ __forceinline__ int part_row(const AttnArgs& a, const Job& j, int key0, int lane, unsigned& bad) {
+  using C = Prefill<D>;
+  const int key = key0 + 16 * lane;
+  if (lane >= C::NSUB || key + 16 <= j.lo || key >= j.hi) return -1;
+  const int id = block_at(a.c, j.b, key >> a.c.log_block, bad);
+  return id < 0 ? -1 : (id * a.c.Hkv + j.kvh) * a.c.block + (key & (a.c.block - 1));
+}
+
+// One warp's share of a tile's codes to fp16: chunks of 256 codes, chunk y =
+// which, which + step, ...; PER at a time, their loads first.  A chunk is part
+// of one 16-key part; parts that are not there become zeros.
+template <int D, int FMT, int PER>
+__device__ __forceinline__ void convert_chunks(const uint8_t* codes, int rows, int y0, int step, uint32_t dst, int lane) {
+  using C = Prefill<D>;
+  constexpr int CHUNKS = C::KT * D / 256, PERPART = D / 16;
+  uint2 w[PER];
+#pragma unroll
+  for (int i = 0; i < PER; ++i) {
+    const int y = y0 + i * step;
+    const int row = __shfl_sync(kAll, rows, y / PERPART & 31);
+    w[i] = make_uint2(0, 0);
+    if (y < CHUNKS && row >= 0)
+      w[i] = __ldg(reinterpret_cast<const uint2*>(codes + static_cast<int64_t>(row) * D + (y % PERPART) * 256 + lane * 8));
+  }
+#pragma unroll
+  for (int i = 0; i < PER; ++i) {
+    const int y = y0 + i * step;
+    if (y < CHUNKS) {
+      uint32_t h[4];
+      codes_to_half2<FMT>(w[i].x, h[0], h[1]);
+      codes_to_half2<FMT>(w[i].y, h[2], h[3]);
+      const int x = y * 32 + lane, r = x / (D / 8), c = x % (D / 8);           // row, 8-channel unit
+      const uint32_t at = dst + (c >> 3) * (C::KT * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4);
+      asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" :: "r"(at), "r"(h[0]), "r"(h[1]), "r"(h[2]), "r"(h[3])
+                   : "memory");
+    }
+  }
+}
+
+template <int D, int FMT>
+__global__ void __launch_bounds__(kThreads, 1) paged_prefill_kernel(AttnArgs a, int nsplit) {
+  using C = Prefill<D>;
+  constexpr int KT = C::KT, NSUB = C::NSUB, ST = C::STAGES;
+  extern __shared__ uint8_t raw_sm[];
+  uint8_t* sm = align_smem_1k(raw_sm);
+  uint8_t* qs = sm;                               // [MT][CB][128 rows][128 B]
+  uint8_t* kbuf = qs + C::QBYTES;                 // [stage][CB][KT rows][128 B]
+  uint8_t* vbuf = kbuf + ST * C::TILE;
+  float4* meta = reinterpret_cast<float4*>(vbuf + ST * C::TILE);               // [4][NSUB]: S_K, log2 S_V, 1 / S_V
+  float* unit = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(meta) + C::META);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(unit + C::ROWS);
+  uint64_t *k_full = bars, *k_empty = bars + ST, *v_full = bars + 2 * ST, *v_empty = bars + 3 * ST;
+  uint64_t *meta_full = bars + 4 * ST, *s_full = meta_full + 4, *p_full = s_full + 2, *o_full = p_full + 2;
+  uint32_t* shared_word = reinterpret_cast<uint32_t*>(bars + C::NBAR);         // the tensor memory's address
+
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  unsigned bad = 0;
+  Job j;
+  if (!find_job<D>(a, nsplit, j, bad)) {
+    if (bad && tid == 0) atomicOr(&g_prefill_fault, bad);
+    return;
+  }
+
+  if (warp == kIssuer) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;"
+                 :: "r"(smem_addr(shared_word)), "n"(C::COLS) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  if (tid == 0) {
+    for (int i = 0; i < ST; ++i) {
+      mbar_init(&k_full[i], 4); mbar_init(&v_full[i], 3);
+      mbar_init(&k_empty[i], 1); mbar_init(&v_empty[i], 1);
+    }
+    for (int i = 0; i < 4; ++i) mbar_init(&meta_full[i], 1);
+    for (int i = 0; i < 2; ++i) { mbar_init(&s_full[i], 1); mbar_init(&p_full[i], 4); mbar_init(&o_full[i], 1); }
+    mbar_fence_init();
+  }
+
+  // ---- the query rows, fp16 with a power of two each, channels in code order
+  for (int r = warp; r < C::ROWS; r += kThreads / 32) {
+    constexpr int PER = D / 128 > 0 ? D / 128 : 1;          // 4-channel groups a lane
+    uint2 w[PER];
+    const bool live = r < j.count;
+    const int row = j.row0 + r, tok = row / a.R;
+    const uint16_t* q = a.q + (j.q0 + static_cast<int64_t>(tok)) * a.q_stride +
+                        static_cast<int64_t>(j.kvh * a.R + row % a.R) * D;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+      const int g = i * 32 + lane;
+      w[i] = live && g < D / 4 ? *reinterpret_cast<const uint2*>(q + 4 * g) : make_uint2(0, 0);
+    }
+    float u = a.scale * kCodeUnit<FMT>;
+    if (a.bf16) {
+      float most = 0.0f;
+#pragma unroll
+      for (int i = 0; i < PER; ++i) {
+        const float2 x = unpack2<true>(w[i].x), y = unpack2<true>(w[i].y);
+        most = fmaxf(most, fmaxf(fmaxf(fabsf(x.x), fabsf(x.y)), fmaxf(fabsf(y.x), fabsf(y.y))));
+      }
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) most = fmaxf(most, __shfl_xor_sync(kAll, most, o));
+      const int k = row_exponent(most);
+      const float up = pow2i(k);
+      u *= pow2i(-k);
+#pragma unroll
+      for (int i = 0; i < PER; ++i) {
+        const float2 x = unpack2<true>(w[i].x), y = unpack2<true>(w[i].y);
+        w[i].x = pack2<false>(x.x * up, x.y * up);
+        w[i].y = pack2<false>(y.x * up, y.y * up);
+      }
+    }
+    const uint32_t sign = a.negative ? 0x80008000u : 0u;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+      const int g = i * 32 + lane;                          // channels 4 g .. 4 g + 3
+      if (g < D / 4) {
+        const uint2 h = make_uint2(__byte_perm(w[i].x, w[i].y, 0x5410) ^ sign, __byte_perm(w[i].x, w[i].y, 0x7632) ^ sign);
+        const int rr = r & 127, cb = g >> 4, un = (g & 15) >> 1;
+        *reinterpret_cast<uint2*>(qs + ((r >> 7) * C::CB + cb) * 16384 + rr * 128 + ((un ^ (rr & 7)) << 4) + (g & 1) * 8) = h;
+      }
+    }
+    if (lane == 0) unit[r] = u;
+  }
+  fence_proxy_async();
+  tmem_fence_before();
+  __syncthreads();
+  tmem_fence_after();
+  const uint32_t tmem = *shared_word;
+  bool ok = true;                                 // this role has met no timeout
+  auto wait_one = [&](uint64_t* bar, uint32_t parity) {
+    if (ok && !mbar_wait(bar, parity, kSpin)) ok = false;
+    return ok;
+  };
+  auto wait = [&](uint64_t* bar, uint32_t parity) {         // a whole warp, of one mind
+    if (ok) ok = __all_sync(kAll, mbar_wait(bar, parity, kSpin));
+    return ok;
+  };
+
+  if (warp < 8) {
+    // ---- softmax
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 176;");
+    const int mt = warp >> 2;
+    if (mt < C::MT) {
+      const int r = mt * 128 + (warp & 3) * 32 + lane;
+      const uint32_t lanes = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
+      const uint32_t o_at = lanes + C::O0 + mt * D;
+      const bool live = r < j.count;
+      const int row = j.row0 + r;
+      const int pos = live ? j.L - j.n + row / a.R : -1;    // this row sees keys .. pos
+      const int low = a.window > 0 ? pos - a.window + 1 : 0;
+      const float u = unit[r];
+      // over the warp: tiles inside [wlow, wpos] need no mask
+      int wpos = pos, wlow = low;
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) {
+        wpos = min(wpos, __shfl_xor_sync(kAll, wpos, o));
+        wlow = max(wlow, __shfl_xor_sync(kAll, wlow, o));
+      }
+      float M = -INFINITY, l = 0.0f;
+      for (int i = 0; i < j.tiles; ++i) {
+        const int sb = C::SB == 2 ? i & 1 : mt;             // score buffer and its barriers
+        const uint32_t s_at = lanes + C::S0 + sb * C::SCOLS;
+        const uint32_t par = C::SB == 2 ? (i >> 1) & 1 : i & 1;
+        if (!wait(&s_full[sb], par) || !wait(&meta_full[i & 3], (i >> 2) & 1)) break;
+        tmem_fence_after();
+        uint32_t s[KT / 32][32];
+#pragma unroll
+        for (int c = 0; c < KT / 32; ++c) tmem_ld32(s[c], s_at + 32 * c);
+        tmem_wait_ld();
+        const float4* sc = meta + (i & 3) * NSUB;
+        const int key0 = j.first + i * KT;
+        if (key0 + KT - 1 > wpos || key0 < wlow) {
+          const int up = pos - key0, down = low - key0;
+#pragma unroll
+          for (int c = 0; c < KT; ++c)
+            if (c > up || c < down) s[c / 32][c % 32] = 0xff800000u;           // -inf
+        }
+        float most = -INFINITY;
+#pragma unroll
+        for (int k = 0; k < NSUB; ++k) {
+          float x = __uint_as_float(s[k / 2][(k & 1) * 16]);
+          x = fmaxf(x, __uint_as_float(s[k / 2][(k & 1) * 16 + 15]));
+#pragma unroll
+          for (int e = 1; e < 15; e += 2)
+            x = max3(x, __uint_as_float(s[k / 2][(k & 1) * 16 + e]), __uint_as_float(s[k / 2][(k & 1) * 16 + e + 1]));
+          const float4 m4 = sc[k];
+          most = fmaxf(most, fmaf(x, fmaxf(u * m4.x, 1e-30f), m4.y));
+        }
+        if (__any_sync(kAll, most > M + kLazy)) {
+          const float now = fmaxf(M, most);
+          const float f = now == -INFINITY ? 1.0f : exp2_approx(M - now);
+          M = now;
+          l *= f;
+          if (i > 0) {                                      // O so far, after its last product
+            if (!wait(&o_full[mt], (i - 1) & 1)) break;
+            tmem_fence_after();
+#pragma unroll 1
+            for (int c = 0; c < D / 32; ++c) {
+              uint32_t o[32];
+              tmem_ld32(o, o_at + 32 * c);
+              tmem_wait_ld();
+#pragma unroll
+              for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+              tmem_st32(o_at + 32 * c, o);
+            }
+          }
+        }
+        const float ref = M == -INFINITY ? 0.0f : kBoost - M;
+#pragma unroll
+        for (int k = 0; k < NSUB; ++k) {
+          const float4 m4 = sc[k];
+          const float ak = fmaxf(u * m4.x, 1e-30f), ck = m4.y + ref;
+          float sum = 0.0f;
+#pragma unroll
+          for (int e = 0; e < 16; e += 2) {
+            const float p0 = exp2_approx(fmaf(__uint_as_float(s[k / 2][(k & 1) * 16 + e]), ak, ck));
+            const float p1 = exp2_approx(fmaf(__uint_as_float(s[k / 2][(k & 1) * 16 + e + 1]), ak, ck));
+            sum += p0 + p1;
+            // weights 16 k + e, e + 1 are word 8 k + e / 2 of the row
+            s[(8 * k + e / 2) / 32][(8 * k + e / 2) % 32] = pack2<false>(p0, p1);
+          }
+          l = fmaf(sum, m4.z, l);
+        }
+#pragma unroll
+        for (int c = 0; c < KT / 64; ++c) tmem_st32(s_at + 32 * c, s[c]);
+        tmem_wait_st();
+        tmem_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&p_full[sb]);
+      }
+      // ---- outputs
+      // (a parity names one of two phases: with two score buffers the last but
+      // one product may still be out, and is waited for first)
+      if (C::SB == 2 && j.tiles > 1) wait(&o_full[mt], j.tiles & 1);
+      if (j.tiles > 0 && wait(&o_full[mt], (j.tiles - 1) & 1)) tmem_fence_after();
+      const bool some = j.tiles > 0 && ok;
+      const float inv = l == 0.0f ? 0.0f : kCodeUnit<FMT> / l;
+      const int64_t token = j.q0 + static_cast<int64_t>(live ? row / a.R : 0);
+      uint16_t* out = a.out + (token * a.c.Hkv * a.R + j.kvh * a.R + (live ? row % a.R : 0)) * D;
+      float* part = nullptr;
+      if (nsplit > 1) part = a.part + ((j.tile * nsplit + j.split) * C::ROWS + r) * (D + 4);
+      if (ok) {
+#pragma unroll 1
+        for (int c = 0; c < D / 32; ++c) {
+          uint32_t o[32];
+          if (some) {
+            tmem_ld32(o, o_at + 32 * c);
+            tmem_wait_ld();
+          } else {
+#pragma unroll
+            for (int e = 0; e < 32; ++e) o[e] = 0;
+          }
+          if (live && nsplit == 1) {
+#pragma unroll
+            for (int e = 0; e < 32; e += 8) {
+              uint32_t h[4];
+#pragma unroll
+              for (int k = 0; k < 2; ++k) {                 // columns hold channels 0, 2, 1, 3 of each four
+                const float x0 = __uint_as_float(o[e + 4 * k]) * inv, x2 = __uint_as_float(o[e + 4 * k + 1]) * inv;
+                const float x1 = __uint_as_float(o[e + 4 * k + 2]) * inv, x3 = __uint_as_float(o[e + 4 * k + 3]) * inv;
+                h[2 * k] = a.bf16 ? pack2<true>(x0, x1) : pack2<false>(x0, x1);
+                h[2 * k + 1] = a.bf16 ? pack2<true>(x2, x3) : pack2<false>(x2, x3);
+              }
+              *reinterpret_cast<uint4*>(out + 32 * c + e) = make_uint4(h[0], h[1], h[2], h[3]);
+            }
+          } else if (live) {
+#pragma unroll
+            for (int e = 0; e < 32; e += 4)
+              *reinterpret_cast<uint4*>(part + 32 * c + e) = make_uint4(o[e], o[e + 2], o[e + 1], o[e + 3]);
+          }
+        }
+        if (live && nsplit > 1) *reinterpret_cast<float2*>(part + D) = make_float2(M, l);
+      }
+      tmem_fence_before();
+    }
+  } else {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
+    if (warp == kIssuer) {
+      // ---- the MMAs
+      if (lane == 0 && j.tiles > 0) {
+        constexpr uint32_t sdesc = kMmaDesc<KT, false>, odesc = kMmaDesc<D, true>;
+        const uint32_t qa = smem_addr(qs), ka = smem_addr(kbuf), va = smem_addr(vbuf);
+        auto scores = [&](int i, int mt, int sb) {
+          const uint32_t kt = ka + (i % ST) * C::TILE;
+#pragma unroll
+          for (int k = 0; k < D / 16; ++k)
+            mma_ss(tmem + C::S0 + sb * C::SCOLS, matrix_desc(qa + (mt * C::CB + k / 4) * 16384 + (k % 4) * 32, 16, 1024),
+                   matrix_desc(kt + (k / 4) * (KT * 128) + (k % 4) * 32, 16, 1024), sdesc, k > 0);
+        };
+        auto values = [&](int i, int mt, int sb) {
+          const uint32_t vt = va + (i % ST) * C::TILE;
+#pragma unroll
+          for (int k = 0; k < KT / 16; ++k)
+            mma_ts(tmem + C::O0 + mt * D, tmem + C::S0 + sb * C::SCOLS + 8 * k,
+                   matrix_desc(vt + k * 2048, KT * 128, 1024), odesc, i > 0 || k > 0);
+        };
+        const int n = j.tiles;
+        if (wait_one(&k_full[0], 0)) {
+          tmem_fence_after();
+          scores(0, 0, 0);
+          mma_commit(&s_full[0]);
+          if constexpr (C::MT == 2) {
+            scores(0, 1, 1);
+            mma_commit(&s_full[1]);
+          }
+          mma_commit(&k_empty[0]);
+        }
+        for (int i = 0; i < n && ok; ++i) {
+          const uint32_t vpar = (i / ST) & 1, kpar = ((i + 1) / ST) & 1;
+          if constexpr (C::MT == 2) {
+            if (!wait_one(&v_full[i % ST], vpar)) break;
+#pragma unroll
+            for (int mt = 0; mt < 2; ++mt) {
+              if (!wait_one(&p_full[mt], i & 1)) break;
+              tmem_fence_after();
+              values(i, mt, mt);
+              mma_commit(&o_full[mt]);
+              if (mt == 1) mma_commit(&v_empty[i % ST]);
+              if (i + 1 < n) {
+                if (mt == 0 && !wait_one(&k_full[(i + 1) % ST], kpar)) break;
+                tmem_fence_after();
+                scores(i + 1, mt, mt);
+                mma_commit(&s_full[mt]);
+                if (mt == 1) mma_commit(&k_empty[(i + 1) % ST]);
+              }
+            }
+          } else {
+            if (i + 1 < n) {
+              if (!wait_one(&k_full[(i + 1) % ST], kpar)) break;
+              tmem_fence_after();
+              scores(i + 1, 0, (i + 1) & 1);
+              mma_commit(&s_full[(i + 1) & 1]);
+              mma_commit(&k_empty[(i + 1) % ST]);
+            }
+            if (!wait_one(&v_full[i % ST], vpar) || !wait_one(&p_full[i & 1], (i >> 1) & 1)) break;
+            tmem_fence_after();
+            values(i, 0, i & 1);
+            mma_commit(&o_full[0]);
+            mma_commit(&v_empty[i % ST]);
+          }
+        }
+      }
+      __syncwarp();
+    } else {
+      // ---- codes to fp16
+      const bool is_v = warp >= kFirstV;
+      const uint8_t* codes = is_v ? a.c.vc : a.c.kc;
+      uint64_t *full = is_v ? v_full : k_full, *empty = is_v ? v_empty : k_empty;
+      const uint32_t base = smem_addr(is_v ? vbuf : kbuf);
+      const int which = is_v ? warp - kFirstV : warp - kFirstK;
+      int rows = j.tiles > 0 ? part_row<D>(a, j, j.first, lane, bad) : -1;
+      for (int i = 0; i < j.tiles; ++i) {
+        const int st = i % ST;
+        float4 m4 = make_float4(0.0f, -INFINITY, 0.0f, 0.0f);        // no block: weights 0
+        if (warp == kFirstK && rows >= 0) {
+          const int x = rows >> a.c.log_block;
+          const float v = fmaxf(a.c.vs[x], kScaleMin);
+          m4 = make_float4(a.c.ks[x], log2f(v), __frcp_rn(v), 0.0f);
+        }
+        if (i >= ST && !wait(&empty[st], (i / ST - 1) & 1)) break;
+        if (warp == kFirstK) {
+          if (lane < NSUB) meta[(i & 3) * NSUB + lane] = m4;
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&meta_full[i & 3]);
+        }
+        const int cur = rows;
+        if (i + 1 < j.tiles) rows = part_row<D>(a, j, j.first + (i + 1) * KT, lane, bad);
+        const uint32_t dst = base + st * C::TILE;
+        constexpr int CHUNKS = KT * D / 256;
+        if (is_v) {
+          constexpr int PER = (CHUNKS + 5) / 6;
+          convert_chunks<D, FMT, PER>(codes, cur, which, 3, dst, lane);
+          convert_chunks<D, FMT, PER>(codes, cur, which + 3 * PER, 3, dst, lane);
+        } else {
+          constexpr int PER = CHUNKS / 8;
+          convert_chunks<D, FMT, PER>(codes, cur, which, 4, dst, lane);
+          convert_chunks<D, FMT, PER>(codes, cur, which + 4 * PER, 4, dst, lane);
+        }
+        fence_proxy_async();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&full[st]);
+      }
+    }
+  }
+  if (!ok) atomicOr(&g_prefill_fault, kFaultWait);
+  if (bad) atomicOr(&g_prefill_fault, bad);
+  tmem_fence_before();
+  __syncthreads();
+  tmem_fence_after();
+  if (warp == kIssuer)
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" :: "r"(tmem), "n"(C::COLS) : "memory");
+}
+
+// ---------------------------------------------------------------------------
+// Join the splits of a tile's rows: a warp per row.
+// ---------------------------------------------------------------------------
+template <int D, int FMT>
+__global__ void __launch_bounds__(256) paged_prefill_join_kernel(AttnArgs a, int nsplit) {
+  using C = Prefill<D>;
+  constexpr int DPL = D / 32, PERTILE = C::ROWS / 8;
+  const int lane = threadIdx.x & 31;
+  const int64_t tile = blockIdx.x / PERTILE;
+  const int r = static_cast<int>(blockIdx.x % PERTILE) * 8 + (threadIdx.x >> 5);
+  const int64_t items = a.total_q * a.R / C::ROWS + a.c.B, item = items - 1 - tile / a.c.Hkv;
+  const int kvh = static_cast<int>(tile % a.c.Hkv);
+  const int b = find_sequence(a.cu, a.c.B, item, a.R, C::ROWS, 1, lane);
+  const int64_t k = item - item_base(a.cu, b, a.R, C::ROWS, 1), c0 = a.cu[b], c1 = a.cu[b + 1];
+  const int64_t row = k * C::ROWS + r;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (c0 < 0 || c1 < c0 || c1 > a.total_q || k < 0 || row >= (c1 - c0) * a.R) return;
+  float o[DPL], m = -INFINITY, l = 0.0f;
+#pragma unroll
+  for (int i = 0; i < DPL; ++i) o[i] = 0.0f;
+  const float* p = a.part + (tile * nsplit * C::ROWS + r) * (D + 4);
+#pragma unroll 4
+  for (int s = 0; s < nsplit; ++s, p += C::ROWS * (D + 4)) {
+    const float2 x = *reinterpret_cast<const float2*>(p + D);
+    const float now = fmaxf(m, x.x), ref = now == -INFINITY ? 0.0f : now;
+    const float e0 = exp2_approx(m - ref), e1 = exp2_approx(x.x - ref);
+    l = l * e0 + x.y * e1;
+#pragma unroll
+    for (int i = 0; i < DPL; i += 2) {
+      const float2 y = *reinterpret_cast<const float2*>(p + lane * DPL + i);
+      o[i] = o[i] * e0 + y.x * e1;
+      o[i + 1] = o[i + 1] * e0 + y.y * e1;
+    }
+    m = now;
+  }
+  const float inv = l == 0.0f ? 0.0f : kCodeUnit<FMT> / l;
+  uint16_t* out = a.out + ((c0 + row / a.R) * a.c.Hkv * a.R + kvh * a.R + row % a.R) * D + lane * DPL;
+#pragma unroll
+  for (int i = 0; i < DPL; i += 2)
+    *reinterpret_cast<uint32_t*>(out + i) = a.bf16 ? pack2<true>(o[i] * inv, o[i + 1] * inv)
+                                                   : pack2<false>(o[i] * inv, o[i + 1] * inv);
+}
+
+template <int D, int FMT>
+cudaError_t launch(const AttnArgs& a, int nsplit, cudaStream_t st) {
+  using C = Prefill<D>;
+  auto k = paged_prefill_kernel<D, FMT>;
+  static std::atomic<int> ready[64];              // the shared-memory opt-in, once per device
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev >= 64 || ready[dev].load(std::memory_order_relaxed) == 0) {
+    e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+    if (e != cudaSuccess) return e;
+    // the roles' register shares (256 x 176 + 256 x 80) are what 128 a thread give
+    cudaFuncAttributes fa;
+    e = cudaFuncGetAttributes(&fa, k);
+    if (e != cudaSuccess) return e;
+    if (fa.numRegs != 128) return cudaErrorInvalidKernelImage;
+    if (dev < 64) ready[dev].store(1, std::memory_order_relaxed);
+  }
+  const int64_t tiles = (a.total_q * a.R / C::ROWS + a.c.B) * a.c.Hkv;
+  k<<<static_cast<unsigned>(tiles * nsplit), kThreads, C::SMEM, st>>>(a, nsplit);
+  e = cudaGetLastError();
+  if (e != cudaSuccess || nsplit == 1) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(tiles * (C::ROWS / 8)));
+  cfg.blockDim = dim3(256);
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, paged_prefill_join_kernel<D, FMT>, a, nsplit);
+}
+
+}  // namespace
+
+__attribute__((visibility("hidden"))) int kvq_paged_prefill_launch(const AttnArgs& a, int format, int nsplit,
+                                                                   cudaStream_t st, cudaError_t& err) {
+  const bool f8 = format == KVQ_E4M3;
+  switch (a.c.D) {
+    case 64: err = f8 ? launch<64, kE4m3>(a, nsplit, st) : launch<64, kInt8>(a, nsplit, st); break;
+    case 128: err = f8 ? launch<128, kE4m3>(a, nsplit, st) : launch<128, kInt8>(a, nsplit, st); break;
+    default: err = f8 ? launch<256, kE4m3>(a, nsplit, st) : launch<256, kInt8>(a, nsplit, st); break;
+  }
+  return err == cudaSuccess ? KVQ_OK : KVQ_ERR_LAUNCH;
+}
+
+__attribute__((visibility("hidden"))) unsigned int kvq_paged_prefill_fault_word(int clear) {
+  unsigned int v = 0;
+  if (cudaMemcpyFromSymbol(&v, g_prefill_fault, sizeof(v)) != cudaSuccess) return 0;
+  if (clear && v) {
+    const unsigned int zero = 0;
+    cudaMemcpyToSymbol(g_prefill_fault, &zero, sizeof(zero));
+  }
+  return v;
+}
