@@ -11,13 +11,13 @@
 // not fill the GPU the keys of a tile are split over several thread blocks,
 // whose partial sums a second kernel joins.
 //
-// A thread block is 16 warps in roles, coupled by mbarriers:
+// A thread block is 17 warps in roles, coupled by mbarriers:
 //   0-7    softmax: a thread per row reads its scores from tensor memory,
 //          makes the weights and writes them back as fp16 (warps 0-3 the first
 //          128 rows, 4-7 the second; at D = 256 only 0-3);
 //   8-11   K: codes from the cache to fp16 in shared memory, 128-byte swizzled;
-//   13-15  V: the same;
-//   12     one thread issues the MMAs (tcgen05, fp16 with fp32 sums in tensor
+//   12-15  V: the same;
+//   16     one thread issues the MMAs (tcgen05, fp16 with fp32 sums in tensor
 //          memory): S = Q K^T from shared memory, O += P V with P from tensor
 //          memory, in an order that gives the tensor cores one tile's products
 //          while the softmax works on the other's (at D = 256: the next keys'
@@ -47,8 +47,8 @@ using namespace kvqp;
 __device__ unsigned int g_prefill_fault = 0;
 
 constexpr uint32_t kSpin = 1u << 22;              // bounded mbarrier waits
-constexpr int kThreads = 512;
-constexpr int kFirstK = 8, kIssuer = 12, kFirstV = 13;     // warps
+constexpr int kThreads = 544;
+constexpr int kFirstK = 8, kFirstV = 12, kIssuer = 16;     // warps
 
 template <int D>
 struct Prefill {
@@ -100,6 +100,14 @@ __device__ __forceinline__ void tmem_st32(uint32_t addr, const uint32_t (&r)[32]
       : "memory");
 }
 
+__device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15};"
+      :: "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
+         "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(addr)
+      : "memory");
+}
+
 // Shared-memory matrix descriptor with the 128-byte swizzle: start address,
 // leading and stride byte offsets in units of 16, descriptor version 1.
 __device__ __forceinline__ uint64_t matrix_desc(uint32_t addr, uint32_t leading, uint32_t stride) {
@@ -110,20 +118,28 @@ __device__ __forceinline__ uint64_t matrix_desc(uint32_t addr, uint32_t leading,
 template <int N, bool B_TRANSPOSED>
 constexpr uint32_t kMmaDesc = (1u << 4) | (B_TRANSPOSED ? 1u << 16 : 0u) | (static_cast<uint32_t>(N >> 3) << 17) |
                               ((128u >> 4) << 24);
-__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t desc, bool add) {
-  asm volatile("{\n.reg .pred p;\nsetp.ne.b32 p, %4, 0;\n"
-               "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}"
-               :: "r"(d), "l"(a), "l"(b), "r"(desc), "r"(static_cast<uint32_t>(add)) : "memory");
+// The whole warp comes here and one thread (`one`) issues: what the warp holds
+// in common stays in uniform registers.
+__device__ __forceinline__ uint32_t elect_one() {
+  uint32_t one;
+  asm volatile("{\n.reg .pred p;\nelect.sync _|p, 0xffffffff;\nselp.u32 %0, 1, 0, p;\n}" : "=r"(one));
+  return one;
 }
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t desc, bool add) {
-  asm volatile("{\n.reg .pred p;\nsetp.ne.b32 p, %4, 0;\n"
-               "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}"
-               :: "r"(d), "r"(a), "l"(b), "r"(desc), "r"(static_cast<uint32_t>(add)) : "memory");
+__device__ __forceinline__ void mma_ss(uint32_t one, uint32_t d, uint64_t a, uint64_t b, uint32_t desc, bool add) {
+  asm volatile("{\n.reg .pred p, q;\nsetp.ne.b32 p, %4, 0;\nsetp.ne.b32 q, %5, 0;\n"
+               "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}"
+               :: "r"(d), "l"(a), "l"(b), "r"(desc), "r"(static_cast<uint32_t>(add)), "r"(one) : "memory");
 }
-// The barrier completes when this thread's MMAs so far have.
-__device__ __forceinline__ void mma_commit(uint64_t* bar) {
-  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];"
-               :: "r"(smem_addr(bar)) : "memory");
+__device__ __forceinline__ void mma_ts(uint32_t one, uint32_t d, uint32_t a, uint64_t b, uint32_t desc, bool add) {
+  asm volatile("{\n.reg .pred p, q;\nsetp.ne.b32 p, %4, 0;\nsetp.ne.b32 q, %5, 0;\n"
+               "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}"
+               :: "r"(d), "r"(a), "l"(b), "r"(desc), "r"(static_cast<uint32_t>(add)), "r"(one) : "memory");
+}
+// The barrier completes when the issuing thread's MMAs so far have.
+__device__ __forceinline__ void mma_commit(uint32_t one, uint64_t* bar) {
+  asm volatile("{\n.reg .pred q;\nsetp.ne.b32 q, %1, 0;\n"
+               "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}"
+               :: "r"(smem_addr(bar)), "r"(one) : "memory");
 }
 
 __device__ __forceinline__ float max3(float a, float b, float c) {
@@ -191,36 +207,45 @@ __device__ __forceinline__ int part_row(const AttnArgs& a, const Job& j, int key
   return id < 0 ? -1 : (id * a.c.Hkv + j.kvh) * a.c.block + (key & (a.c.block - 1));
 }
 
-// One warp's share of a tile's codes to fp16: chunks of 256 codes, chunk y =
-// which, which + step, ...; PER at a time, their loads first.  A chunk is part
-// of one 16-key part; parts that are not there become zeros.
-template <int D, int FMT, int PER>
-__device__ __forceinline__ void convert_chunks(const uint8_t* codes, int rows, int y0, int step, uint32_t dst, int lane) {
+// One of four warps' share of a tile's codes: chunks of 256 codes (32 lanes of
+// 8), chunk 4 i + which for i < N.  Chunk 4 i + which lies in part
+// 4 i / (D / 16), since which < 4, and parts that are not there become zeros.
+template <int D>
+struct Share {
   using C = Prefill<D>;
-  constexpr int CHUNKS = C::KT * D / 256, PERPART = D / 16;
-  uint2 w[PER];
+  static constexpr int N = C::KT * D / 1024;
+  static constexpr int PERPART = D / 16;          // chunks of a 16-key part
+  uint2 w[N];
+  __device__ __forceinline__ void load(const uint8_t* codes, int rows, int which, int lane) {
+    const uint8_t* mine = codes + which * 256 + lane * 8;
+    const uint8_t* p = nullptr;
 #pragma unroll
-  for (int i = 0; i < PER; ++i) {
-    const int y = y0 + i * step;
-    const int row = __shfl_sync(kAll, rows, y / PERPART & 31);
-    w[i] = make_uint2(0, 0);
-    if (y < CHUNKS && row >= 0)
-      w[i] = __ldg(reinterpret_cast<const uint2*>(codes + static_cast<int64_t>(row) * D + (y % PERPART) * 256 + lane * 8));
+    for (int i = 0; i < N; ++i) {
+      if (4 * i % PERPART == 0) {                 // a part's first chunk
+        const int row = __shfl_sync(kAll, rows, 4 * i / PERPART);
+        p = row < 0 ? nullptr : mine + static_cast<int64_t>(row) * D;
+      }
+      w[i] = p ? __ldg(reinterpret_cast<const uint2*>(p + 4 * i % PERPART * 256)) : make_uint2(0, 0);
+    }
   }
+  // To the tile at dst: row r, 8-channel unit c at unit (c mod 8) ^ (r mod 8) of
+  // row r of block c / 8.  From one chunk to the next the row grows by 1024 / D,
+  // which changes r mod 8 at D = 256 only, by 4.
+  template <int FMT>
+  __device__ __forceinline__ void store(uint32_t dst, int which, int lane) const {
+    const int x = which * 32 + lane, r = x / (D / 8), c = x % (D / 8);
+    const uint32_t at = dst + (c >> 3) * (C::KT * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4);
 #pragma unroll
-  for (int i = 0; i < PER; ++i) {
-    const int y = y0 + i * step;
-    if (y < CHUNKS) {
+    for (int i = 0; i < N; ++i) {
       uint32_t h[4];
       codes_to_half2<FMT>(w[i].x, h[0], h[1]);
       codes_to_half2<FMT>(w[i].y, h[2], h[3]);
-      const int x = y * 32 + lane, r = x / (D / 8), c = x % (D / 8);           // row, 8-channel unit
-      const uint32_t at = dst + (c >> 3) * (C::KT * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4);
-      asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" :: "r"(at), "r"(h[0]), "r"(h[1]), "r"(h[2]), "r"(h[3])
+      const uint32_t to = (D == 256 && (i & 1) ? at ^ 64u : at) + i * (1024 / D * 128);
+      asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" :: "r"(to), "r"(h[0]), "r"(h[1]), "r"(h[2]), "r"(h[3])
                    : "memory");
     }
   }
-}
+};
 
 template <int D, int FMT>
 __global__ void __launch_bounds__(kThreads, 1) paged_prefill_kernel(AttnArgs a, int nsplit) {
@@ -253,7 +278,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_prefill_kernel(AttnArgs a, 
   }
   if (tid == 0) {
     for (int i = 0; i < ST; ++i) {
-      mbar_init(&k_full[i], 4); mbar_init(&v_full[i], 3);
+      mbar_init(&k_full[i], 4); mbar_init(&v_full[i], 4);
       mbar_init(&k_empty[i], 1); mbar_init(&v_empty[i], 1);
     }
     for (int i = 0; i < 4; ++i) mbar_init(&meta_full[i], 1);
@@ -312,10 +337,6 @@ __global__ void __launch_bounds__(kThreads, 1) paged_prefill_kernel(AttnArgs a, 
   tmem_fence_after();
   const uint32_t tmem = *shared_word;
   bool ok = true;                                 // this role has met no timeout
-  auto wait_one = [&](uint64_t* bar, uint32_t parity) {
-    if (ok && !mbar_wait(bar, parity, kSpin)) ok = false;
-    return ok;
-  };
   auto wait = [&](uint64_t* bar, uint32_t parity) {         // a whole warp, of one mind
     if (ok) ok = __all_sync(kAll, mbar_wait(bar, parity, kSpin));
     return ok;
@@ -323,7 +344,6 @@ __global__ void __launch_bounds__(kThreads, 1) paged_prefill_kernel(AttnArgs a, 
 
   if (warp < 8) {
     // ---- softmax
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 176;");
     const int mt = warp >> 2;
     if (mt < C::MT) {
       const int r = mt * 128 + (warp & 3) * 32 + lane;
@@ -348,28 +368,35 @@ __global__ void __launch_bounds__(kThreads, 1) paged_prefill_kernel(AttnArgs a, 
         const uint32_t par = C::SB == 2 ? (i >> 1) & 1 : i & 1;
         if (!wait(&s_full[sb], par) || !wait(&meta_full[i & 3], (i >> 2) & 1)) break;
         tmem_fence_after();
-        uint32_t s[KT / 32][32];
-#pragma unroll
-        for (int c = 0; c < KT / 32; ++c) tmem_ld32(s[c], s_at + 32 * c);
-        tmem_wait_ld();
         const float4* sc = meta + (i & 3) * NSUB;
         const int key0 = j.first + i * KT;
-        if (key0 + KT - 1 > wpos || key0 < wlow) {
-          const int up = pos - key0, down = low - key0;
+        const bool edge = key0 + KT - 1 > wpos || key0 < wlow;
+        const int up = pos - key0, down = low - key0;       // columns down .. up are seen
+        // 32 columns of scores; twice, for the maximum and for the weights:
+        // tensor memory has the bandwidth, and a thread keeps few registers
+        auto load = [&](uint32_t (&s)[32], int c) {
+          tmem_ld32(s, s_at + 32 * c);
+          tmem_wait_ld();
+          if (edge) {
 #pragma unroll
-          for (int c = 0; c < KT; ++c)
-            if (c > up || c < down) s[c / 32][c % 32] = 0xff800000u;           // -inf
-        }
+            for (int e = 0; e < 32; ++e)
+              if (32 * c + e > up || 32 * c + e < down) s[e] = 0xff800000u;           // -inf
+          }
+        };
         float most = -INFINITY;
+#pragma unroll 1
+        for (int c = 0; c < KT / 32; ++c) {
+          uint32_t s[32];
+          load(s, c);
 #pragma unroll
-        for (int k = 0; k < NSUB; ++k) {
-          float x = __uint_as_float(s[k / 2][(k & 1) * 16]);
-          x = fmaxf(x, __uint_as_float(s[k / 2][(k & 1) * 16 + 15]));
+          for (int k = 0; k < 2; ++k) {
+            float x = fmaxf(__uint_as_float(s[16 * k]), __uint_as_float(s[16 * k + 15]));
 #pragma unroll
-          for (int e = 1; e < 15; e += 2)
-            x = max3(x, __uint_as_float(s[k / 2][(k & 1) * 16 + e]), __uint_as_float(s[k / 2][(k & 1) * 16 + e + 1]));
-          const float4 m4 = sc[k];
-          most = fmaxf(most, fmaf(x, fmaxf(u * m4.x, 1e-30f), m4.y));
+            for (int e = 1; e < 15; e += 2)
+              x = max3(x, __uint_as_float(s[16 * k + e]), __uint_as_float(s[16 * k + e + 1]));
+            const float4 m4 = sc[2 * c + k];
+            most = fmaxf(most, fmaf(x, fmaxf(u * m4.x, 1e-30f), m4.y));
+          }
         }
         if (__any_sync(kAll, most > M + kLazy)) {
           const float now = fmaxf(M, most);
@@ -391,23 +418,30 @@ __global__ void __launch_bounds__(kThreads, 1) paged_prefill_kernel(AttnArgs a, 
           }
         }
         const float ref = M == -INFINITY ? 0.0f : kBoost - M;
+#pragma unroll 1
+        for (int c = 0; c < KT / 32; ++c) {
+          uint32_t s[32], w[16];
+          load(s, c);
 #pragma unroll
-        for (int k = 0; k < NSUB; ++k) {
-          const float4 m4 = sc[k];
-          const float ak = fmaxf(u * m4.x, 1e-30f), ck = m4.y + ref;
-          float sum = 0.0f;
+          for (int k = 0; k < 2; ++k) {
+            const float4 m4 = sc[2 * c + k];
+            const float ak = fmaxf(u * m4.x, 1e-30f), ck = m4.y + ref;
+            const float2 a2 = make_float2(ak, ak), c2 = make_float2(ck, ck);
+            float2 sum = make_float2(0.0f, 0.0f);
 #pragma unroll
-          for (int e = 0; e < 16; e += 2) {
-            const float p0 = exp2_approx(fmaf(__uint_as_float(s[k / 2][(k & 1) * 16 + e]), ak, ck));
-            const float p1 = exp2_approx(fmaf(__uint_as_float(s[k / 2][(k & 1) * 16 + e + 1]), ak, ck));
-            sum += p0 + p1;
-            // weights 16 k + e, e + 1 are word 8 k + e / 2 of the row
-            s[(8 * k + e / 2) / 32][(8 * k + e / 2) % 32] = pack2<false>(p0, p1);
+            for (int e = 0; e < 16; e += 2) {
+              const float2 x = make_float2(__uint_as_float(s[16 * k + e]), __uint_as_float(s[16 * k + e + 1]));
+              float2 p = __ffma2_rn(x, a2, c2);
+              p.x = exp2_approx(p.x);
+              p.y = exp2_approx(p.y);
+              sum = __fadd2_rn(sum, p);
+              w[8 * k + e / 2] = pack2<false>(p.x, p.y);
+            }
+            l = fmaf(sum.x + sum.y, m4.z, l);
           }
-          l = fmaf(sum, m4.z, l);
+          // weights 32 c .. are columns 16 c .., behind the scores still to be read
+          tmem_st16(s_at + 16 * c, w);
         }
-#pragma unroll
-        for (int c = 0; c < KT / 64; ++c) tmem_st32(s_at + 32 * c, s[c]);
         tmem_wait_st();
         tmem_fence_before();
         __syncwarp();
@@ -459,81 +493,91 @@ __global__ void __launch_bounds__(kThreads, 1) paged_prefill_kernel(AttnArgs a, 
       tmem_fence_before();
     }
   } else {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
     if (warp == kIssuer) {
       // ---- the MMAs
-      if (lane == 0 && j.tiles > 0) {
+      if (j.tiles > 0) {
         constexpr uint32_t sdesc = kMmaDesc<KT, false>, odesc = kMmaDesc<D, true>;
-        const uint32_t qa = smem_addr(qs), ka = smem_addr(kbuf), va = smem_addr(vbuf);
+        const uint32_t one = elect_one();
+        const uint64_t qd = matrix_desc(smem_addr(qs), 16, 1024), kd = matrix_desc(smem_addr(kbuf), 16, 1024);
+        const uint64_t vd = matrix_desc(smem_addr(vbuf), KT * 128, 1024);
+        // (start addresses count in 16 bytes)
         auto scores = [&](int i, int mt, int sb) {
-          const uint32_t kt = ka + (i % ST) * C::TILE;
+          const uint64_t kt = kd + (i % ST) * (C::TILE / 16);
 #pragma unroll
           for (int k = 0; k < D / 16; ++k)
-            mma_ss(tmem + C::S0 + sb * C::SCOLS, matrix_desc(qa + (mt * C::CB + k / 4) * 16384 + (k % 4) * 32, 16, 1024),
-                   matrix_desc(kt + (k / 4) * (KT * 128) + (k % 4) * 32, 16, 1024), sdesc, k > 0);
+            mma_ss(one, tmem + C::S0 + sb * C::SCOLS, qd + (mt * C::CB + k / 4) * (16384 / 16) + (k % 4) * 2,
+                   kt + (k / 4) * (KT * 128 / 16) + (k % 4) * 2, sdesc, k > 0);
         };
         auto values = [&](int i, int mt, int sb) {
-          const uint32_t vt = va + (i % ST) * C::TILE;
+          const uint64_t vt = vd + (i % ST) * (C::TILE / 16);
 #pragma unroll
           for (int k = 0; k < KT / 16; ++k)
-            mma_ts(tmem + C::O0 + mt * D, tmem + C::S0 + sb * C::SCOLS + 8 * k,
-                   matrix_desc(vt + k * 2048, KT * 128, 1024), odesc, i > 0 || k > 0);
+            mma_ts(one, tmem + C::O0 + mt * D, tmem + C::S0 + sb * C::SCOLS + 8 * k, vt + k * (2048 / 16), odesc,
+                   i > 0 || k > 0);
         };
         const int n = j.tiles;
-        if (wait_one(&k_full[0], 0)) {
+        if (wait(&k_full[0], 0)) {
           tmem_fence_after();
           scores(0, 0, 0);
-          mma_commit(&s_full[0]);
+          mma_commit(one, &s_full[0]);
           if constexpr (C::MT == 2) {
             scores(0, 1, 1);
-            mma_commit(&s_full[1]);
+            mma_commit(one, &s_full[1]);
           }
-          mma_commit(&k_empty[0]);
+          mma_commit(one, &k_empty[0]);
         }
+#pragma unroll 1
         for (int i = 0; i < n && ok; ++i) {
           const uint32_t vpar = (i / ST) & 1, kpar = ((i + 1) / ST) & 1;
           if constexpr (C::MT == 2) {
-            if (!wait_one(&v_full[i % ST], vpar)) break;
+            if (!wait(&v_full[i % ST], vpar)) break;
 #pragma unroll
             for (int mt = 0; mt < 2; ++mt) {
-              if (!wait_one(&p_full[mt], i & 1)) break;
+              if (!wait(&p_full[mt], i & 1)) break;
               tmem_fence_after();
               values(i, mt, mt);
-              mma_commit(&o_full[mt]);
-              if (mt == 1) mma_commit(&v_empty[i % ST]);
+              mma_commit(one, &o_full[mt]);
+              if (mt == 1) mma_commit(one, &v_empty[i % ST]);
               if (i + 1 < n) {
-                if (mt == 0 && !wait_one(&k_full[(i + 1) % ST], kpar)) break;
+                if (mt == 0 && !wait(&k_full[(i + 1) % ST], kpar)) break;
                 tmem_fence_after();
                 scores(i + 1, mt, mt);
-                mma_commit(&s_full[mt]);
-                if (mt == 1) mma_commit(&k_empty[(i + 1) % ST]);
+                mma_commit(one, &s_full[mt]);
+                if (mt == 1) mma_commit(one, &k_empty[(i + 1) % ST]);
               }
             }
           } else {
             if (i + 1 < n) {
-              if (!wait_one(&k_full[(i + 1) % ST], kpar)) break;
+              if (!wait(&k_full[(i + 1) % ST], kpar)) break;
               tmem_fence_after();
               scores(i + 1, 0, (i + 1) & 1);
-              mma_commit(&s_full[(i + 1) & 1]);
-              mma_commit(&k_empty[(i + 1) % ST]);
+              mma_commit(one, &s_full[(i + 1) & 1]);
+              mma_commit(one, &k_empty[(i + 1) % ST]);
             }
-            if (!wait_one(&v_full[i % ST], vpar) || !wait_one(&p_full[i & 1], (i >> 1) & 1)) break;
+            if (!wait(&v_full[i % ST], vpar) || !wait(&p_full[i & 1], (i >> 1) & 1)) break;
             tmem_fence_after();
             values(i, 0, i & 1);
-            mma_commit(&o_full[0]);
-            mma_commit(&v_empty[i % ST]);
+            mma_commit(one, &o_full[0]);
+            mma_commit(one, &v_empty[i % ST]);
           }
         }
       }
-      __syncwarp();
     } else {
-      // ---- codes to fp16
+      // ---- codes to fp16, the next tile's loads in flight over this one's
+      // conversion and wait
       const bool is_v = warp >= kFirstV;
       const uint8_t* codes = is_v ? a.c.vc : a.c.kc;
       uint64_t *full = is_v ? v_full : k_full, *empty = is_v ? v_empty : k_empty;
       const uint32_t base = smem_addr(is_v ? vbuf : kbuf);
-      const int which = is_v ? warp - kFirstV : warp - kFirstK;
-      int rows = j.tiles > 0 ? part_row<D>(a, j, j.first, lane, bad) : -1;
+      const int which = (warp - kFirstK) & 3;
+      Share<D> next;
+      int rows = -1, rows2 = -1;                  // the parts of the tile in `next`, and of the one after it
+      if (j.tiles > 0) {
+        rows = part_row<D>(a, j, j.first, lane, bad);
+        next.load(codes, rows, which, lane);
+        if (j.tiles > 1) rows2 = part_row<D>(a, j, j.first + KT, lane, bad);
+      }
+#pragma unroll 1
       for (int i = 0; i < j.tiles; ++i) {
         const int st = i % ST;
         float4 m4 = make_float4(0.0f, -INFINITY, 0.0f, 0.0f);        // no block: weights 0
@@ -548,22 +592,13 @@ __global__ void __launch_bounds__(kThreads, 1) paged_prefill_kernel(AttnArgs a, 
           __syncwarp();
           if (lane == 0) mbar_arrive(&meta_full[i & 3]);
         }
-        const int cur = rows;
-        if (i + 1 < j.tiles) rows = part_row<D>(a, j, j.first + (i + 1) * KT, lane, bad);
-        const uint32_t dst = base + st * C::TILE;
-        constexpr int CHUNKS = KT * D / 256;
-        if (is_v) {
-          constexpr int PER = (CHUNKS + 5) / 6;
-          convert_chunks<D, FMT, PER>(codes, cur, which, 3, dst, lane);
-          convert_chunks<D, FMT, PER>(codes, cur, which + 3 * PER, 3, dst, lane);
-        } else {
-          constexpr int PER = CHUNKS / 8;
-          convert_chunks<D, FMT, PER>(codes, cur, which, 4, dst, lane);
-          convert_chunks<D, FMT, PER>(codes, cur, which + 4 * PER, 4, dst, lane);
-        }
+        next.template store<FMT>(base + st * C::TILE, which, lane);
         fence_proxy_async();
         __syncwarp();
         if (lane == 0) mbar_arrive(&full[st]);
+        rows = rows2;
+        if (i + 1 < j.tiles) next.load(codes, rows, which, lane);
+        if (i + 2 < j.tiles) rows2 = part_row<D>(a, j, j.first + (i + 2) * KT, lane, bad);
       }
     }
   }
@@ -630,11 +665,6 @@ cudaError_t launch(const AttnArgs& a, int nsplit, cudaStream_t st) {
   if (dev >= 64 || ready[dev].load(std::memory_order_relaxed) == 0) {
     e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
     if (e != cudaSuccess) return e;
-    // the roles' register shares (256 x 176 + 256 x 80) are what 128 a thread give
-    cudaFuncAttributes fa;
-    e = cudaFuncGetAttributes(&fa, k);
-    if (e != cudaSuccess) return e;
-    if (fa.numRegs != 128) return cudaErrorInvalidKernelImage;
     if (dev < 64) ready[dev].store(1, std::memory_order_relaxed);
   }
   const int64_t tiles = (a.total_q * a.R / C::ROWS + a.c.B) * a.c.Hkv;
