@@ -19,9 +19,9 @@
 //   12-15  V: the same;
 //   16     one thread issues the MMAs (tcgen05, fp16 with fp32 sums in tensor
 //          memory): S = Q K^T from shared memory, O += P V with P from tensor
-//          memory, in an order that gives the tensor cores one tile's products
-//          while the softmax works on the other's (at D = 256: the next keys'
-//          scores while it works on these).
+//          memory, 64 keys a step.  Each 128 rows have two score buffers: the
+//          scores two steps on are asked for as soon as a step's weights are
+//          there, so the softmax, which bounds the loop, never waits for them.
 // Codes are exact in fp16, so K and V are converted once per thread block and
 // tile; their scales are in the softmax's exponent.  Code pairs unpack as
 // channels (0, 2), (1, 3): Q's channels are laid out in that order too, and the
@@ -47,14 +47,19 @@ using namespace kvqp;
 __device__ unsigned int g_prefill_fault = 0;
 
 constexpr uint32_t kSpin = 1u << 22;              // bounded mbarrier waits
-constexpr int kThreads = 544;
+constexpr int kStep = 64;                         // keys of one softmax step
+constexpr int kThreads = 640;                    // 17 warps in roles, in five warpgroups
 constexpr int kFirstK = 8, kFirstV = 12, kIssuer = 16;     // warps
+// Registers a thread by role.  Together they must not exceed what the block is
+// launched with: 256 x 128 + 256 x 80 + 128 x 64 = 61,440 of 640 x 96.
+constexpr int kSoftmaxRegs = 128, kConvertRegs = 80, kIssuerRegs = 64;
+constexpr int kRegsNeeded = 256 * kSoftmaxRegs + 256 * kConvertRegs + 128 * kIssuerRegs;
 
 template <int D>
 struct Prefill {
   static constexpr int MT = D == 256 ? 1 : 2;     // 128-row tiles
-  static constexpr int SB = D == 256 ? 2 : 1;     // score buffers of one of them
-  static constexpr int KT = D == 256 ? 64 : 128;  // keys of a tile
+  static constexpr int KT = D == 256 ? 64 : 128;  // keys of a tile in shared memory
+  static constexpr int STEPS = KT / kStep;        // steps of a tile
   static constexpr int ROWS = MT * 128;
   static constexpr int CB = D / 64;               // 64-channel blocks (128-byte swizzled rows)
   static constexpr int NSUB = KT / 16;            // 16-key parts, each inside one cache block
@@ -62,10 +67,11 @@ struct Prefill {
   static constexpr int TILE = KT * D * 2;         // fp16 bytes of a K or V tile
   static constexpr int STAGES = 2;
   static constexpr int META = 4 * NSUB * 16;      // scales of four tiles
-  static constexpr int NBAR = 4 * STAGES + 4 + 2 * 2 + 2;
+  static constexpr int NBAR = 4 * STAGES + 4 + 3 * 4;
   static constexpr int SMEM = 1024 + QBYTES + 2 * STAGES * TILE + META + ROWS * 4 + NBAR * 8 + 64;
-  // tensor memory columns: scores (and weights over them), then outputs
-  static constexpr int S0 = 0, SCOLS = KT, O0 = 2 * SCOLS;
+  // tensor memory columns: two score buffers (the weights over them) for each
+  // 128 rows, then the outputs
+  static constexpr int O0 = MT * 2 * kStep;
   static constexpr uint32_t COLS = 512;
 };
 
@@ -97,14 +103,6 @@ __device__ __forceinline__ void tmem_st32(uint32_t addr, const uint32_t (&r)[32]
          "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]),
          "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]),
          "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31]), "r"(addr)
-      : "memory");
-}
-
-__device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t (&r)[16]) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15};"
-      :: "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
-         "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(addr)
       : "memory");
 }
 
@@ -154,7 +152,7 @@ struct Job {
   int b, kvh, n, L;
   int row0, count, q0;        // q0: the sequence's first row in the packed queries
   int lo, hi;                 // keys that some row sees
-  int first, tiles;           // first key of the first tile; tiles of this split
+  int first, tiles, steps;    // first key of the first tile; tiles and steps of this split
   int split;
   int64_t tile;               // the tile's number, for partial sums
 };
@@ -193,6 +191,7 @@ __device__ __forceinline__ bool find_job(const AttnArgs& a, int nsplit, Job& j, 
   const int t1 = static_cast<int>(static_cast<int64_t>(tiles) * (j.split + 1) / nsplit);
   j.first += t0 * C::KT;
   j.tiles = t1 - t0;
+  j.steps = j.tiles > 0 ? min(j.tiles * C::STEPS, (j.hi - j.first + kStep - 1) / kStep) : 0;
   return true;
 }
 
@@ -260,7 +259,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_prefill_kernel(AttnArgs a, 
   float* unit = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(meta) + C::META);
   uint64_t* bars = reinterpret_cast<uint64_t*>(unit + C::ROWS);
   uint64_t *k_full = bars, *k_empty = bars + ST, *v_full = bars + 2 * ST, *v_empty = bars + 3 * ST;
-  uint64_t *meta_full = bars + 4 * ST, *s_full = meta_full + 4, *p_full = s_full + 2, *o_full = p_full + 2;
+  uint64_t *meta_full = bars + 4 * ST, *s_full = meta_full + 4, *p_full = s_full + 4, *o_full = p_full + 4;
   uint32_t* shared_word = reinterpret_cast<uint32_t*>(bars + C::NBAR);         // the tensor memory's address
 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -282,7 +281,9 @@ __global__ void __launch_bounds__(kThreads, 1) paged_prefill_kernel(AttnArgs a, 
       mbar_init(&k_empty[i], 1); mbar_init(&v_empty[i], 1);
     }
     for (int i = 0; i < 4; ++i) mbar_init(&meta_full[i], 1);
-    for (int i = 0; i < 2; ++i) { mbar_init(&s_full[i], 1); mbar_init(&p_full[i], 4); mbar_init(&o_full[i], 1); }
+    // per 128 rows, steps alternate between two of each: a wait is then never two
+    // phases behind, which a parity could not tell from none
+    for (int i = 0; i < 4; ++i) { mbar_init(&s_full[i], 1); mbar_init(&p_full[i], 4); mbar_init(&o_full[i], 1); }
     mbar_fence_init();
   }
 
@@ -344,6 +345,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_prefill_kernel(AttnArgs a, 
 
   if (warp < 8) {
     // ---- softmax
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" :: "n"(kSoftmaxRegs));
     const int mt = warp >> 2;
     if (mt < C::MT) {
       const int r = mt * 128 + (warp & 3) * 32 + lane;
@@ -362,41 +364,33 @@ __global__ void __launch_bounds__(kThreads, 1) paged_prefill_kernel(AttnArgs a, 
         wlow = max(wlow, __shfl_xor_sync(kAll, wlow, o));
       }
       float M = -INFINITY, l = 0.0f;
-      for (int i = 0; i < j.tiles; ++i) {
-        const int sb = C::SB == 2 ? i & 1 : mt;             // score buffer and its barriers
-        const uint32_t s_at = lanes + C::S0 + sb * C::SCOLS;
-        const uint32_t par = C::SB == 2 ? (i >> 1) & 1 : i & 1;
-        if (!wait(&s_full[sb], par) || !wait(&meta_full[i & 3], (i >> 2) & 1)) break;
-        tmem_fence_after();
-        const float4* sc = meta + (i & 3) * NSUB;
-        const int key0 = j.first + i * KT;
-        const bool edge = key0 + KT - 1 > wpos || key0 < wlow;
-        const int up = pos - key0, down = low - key0;       // columns down .. up are seen
-        // 32 columns of scores; twice, for the maximum and for the weights:
-        // tensor memory has the bandwidth, and a thread keeps few registers
-        auto load = [&](uint32_t (&s)[32], int c) {
-          tmem_ld32(s, s_at + 32 * c);
-          tmem_wait_ld();
-          if (edge) {
-#pragma unroll
-            for (int e = 0; e < 32; ++e)
-              if (32 * c + e > up || 32 * c + e < down) s[e] = 0xff800000u;           // -inf
-          }
-        };
-        float most = -INFINITY;
 #pragma unroll 1
-        for (int c = 0; c < KT / 32; ++c) {
-          uint32_t s[32];
-          load(s, c);
+      for (int i = 0; i < j.steps; ++i) {
+        const int buf = mt * 2 + (i & 1), tile = i / C::STEPS;
+        const uint32_t s_at = lanes + buf * kStep;
+        if (!wait(&s_full[buf], (i >> 1) & 1) || !wait(&meta_full[tile & 3], (tile >> 2) & 1)) break;
+        tmem_fence_after();
+        uint32_t s[2][32];
+        tmem_ld32(s[0], s_at);
+        tmem_ld32(s[1], s_at + 32);
+        tmem_wait_ld();
+        const float4* sc = meta + (tile & 3) * NSUB + (C::STEPS == 2 ? (i & 1) * 4 : 0);
+        const int key0 = j.first + i * kStep;
+        if (key0 + kStep - 1 > wpos || key0 < wlow) {
+          const int up = pos - key0, down = low - key0;     // columns down .. up are seen
 #pragma unroll
-          for (int k = 0; k < 2; ++k) {
-            float x = fmaxf(__uint_as_float(s[16 * k]), __uint_as_float(s[16 * k + 15]));
+          for (int c = 0; c < kStep; ++c)
+            if (c > up || c < down) s[c / 32][c % 32] = 0xff800000u;       // -inf
+        }
+        auto at = [&](int c) { return __uint_as_float(s[c / 32][c % 32]); };
+        float most = -INFINITY;
 #pragma unroll
-            for (int e = 1; e < 15; e += 2)
-              x = max3(x, __uint_as_float(s[16 * k + e]), __uint_as_float(s[16 * k + e + 1]));
-            const float4 m4 = sc[2 * c + k];
-            most = fmaxf(most, fmaf(x, fmaxf(u * m4.x, 1e-30f), m4.y));
-          }
+        for (int k = 0; k < kStep / 16; ++k) {
+          float x = fmaxf(at(16 * k), at(16 * k + 15));
+#pragma unroll
+          for (int e = 1; e < 15; e += 2) x = max3(x, at(16 * k + e), at(16 * k + e + 1));
+          const float4 m4 = sc[k];
+          most = fmaxf(most, fmaf(x, fmaxf(u * m4.x, 1e-30f), m4.y));
         }
         if (__any_sync(kAll, most > M + kLazy)) {
           const float now = fmaxf(M, most);
@@ -404,7 +398,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_prefill_kernel(AttnArgs a, 
           M = now;
           l *= f;
           if (i > 0) {                                      // O so far, after its last product
-            if (!wait(&o_full[mt], (i - 1) & 1)) break;
+            if (!wait(&o_full[mt * 2 + ((i - 1) & 1)], ((i - 1) >> 1) & 1)) break;
             tmem_fence_after();
 #pragma unroll 1
             for (int c = 0; c < D / 32; ++c) {
@@ -418,41 +412,32 @@ __global__ void __launch_bounds__(kThreads, 1) paged_prefill_kernel(AttnArgs a, 
           }
         }
         const float ref = M == -INFINITY ? 0.0f : kBoost - M;
-#pragma unroll 1
-        for (int c = 0; c < KT / 32; ++c) {
-          uint32_t s[32], w[16];
-          load(s, c);
+        uint32_t w[32];
 #pragma unroll
-          for (int k = 0; k < 2; ++k) {
-            const float4 m4 = sc[2 * c + k];
-            const float ak = fmaxf(u * m4.x, 1e-30f), ck = m4.y + ref;
-            const float2 a2 = make_float2(ak, ak), c2 = make_float2(ck, ck);
-            float2 sum = make_float2(0.0f, 0.0f);
+        for (int k = 0; k < kStep / 16; ++k) {
+          const float4 m4 = sc[k];
+          const float ak = fmaxf(u * m4.x, 1e-30f), ck = m4.y + ref;
+          const float2 a2 = make_float2(ak, ak), c2 = make_float2(ck, ck);
+          float2 sum = make_float2(0.0f, 0.0f);
 #pragma unroll
-            for (int e = 0; e < 16; e += 2) {
-              const float2 x = make_float2(__uint_as_float(s[16 * k + e]), __uint_as_float(s[16 * k + e + 1]));
-              float2 p = __ffma2_rn(x, a2, c2);
-              p.x = exp2_approx(p.x);
-              p.y = exp2_approx(p.y);
-              sum = __fadd2_rn(sum, p);
-              w[8 * k + e / 2] = pack2<false>(p.x, p.y);
-            }
-            l = fmaf(sum.x + sum.y, m4.z, l);
+          for (int e = 0; e < 16; e += 2) {
+            float2 p = __ffma2_rn(make_float2(at(16 * k + e), at(16 * k + e + 1)), a2, c2);
+            p.x = exp2_approx(p.x);
+            p.y = exp2_approx(p.y);
+            sum = __fadd2_rn(sum, p);
+            w[8 * k + e / 2] = pack2<false>(p.x, p.y);
           }
-          // weights 32 c .. are columns 16 c .., behind the scores still to be read
-          tmem_st16(s_at + 16 * c, w);
+          l = fmaf(sum.x + sum.y, m4.z, l);
         }
+        tmem_st32(s_at, w);
         tmem_wait_st();
         tmem_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&p_full[sb]);
+        if (lane == 0) mbar_arrive(&p_full[buf]);
       }
       // ---- outputs
-      // (a parity names one of two phases: with two score buffers the last but
-      // one product may still be out, and is waited for first)
-      if (C::SB == 2 && j.tiles > 1) wait(&o_full[mt], j.tiles & 1);
-      if (j.tiles > 0 && wait(&o_full[mt], (j.tiles - 1) & 1)) tmem_fence_after();
-      const bool some = j.tiles > 0 && ok;
+      if (j.steps > 0 && wait(&o_full[mt * 2 + ((j.steps - 1) & 1)], ((j.steps - 1) >> 1) & 1)) tmem_fence_after();
+      const bool some = j.steps > 0 && ok;
       const float inv = l == 0.0f ? 0.0f : kCodeUnit<FMT> / l;
       const int64_t token = j.q0 + static_cast<int64_t>(live ? row / a.R : 0);
       uint16_t* out = a.out + (token * a.c.Hkv * a.R + j.kvh * a.R + (live ? row % a.R : 0)) * D;
@@ -492,77 +477,72 @@ __global__ void __launch_bounds__(kThreads, 1) paged_prefill_kernel(AttnArgs a, 
       }
       tmem_fence_before();
     }
-  } else {
-    if (warp == kIssuer) {
+  } else if (warp >= kIssuer) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" :: "n"(kIssuerRegs));
+    {
       // ---- the MMAs
-      if (j.tiles > 0) {
-        constexpr uint32_t sdesc = kMmaDesc<KT, false>, odesc = kMmaDesc<D, true>;
+      if (warp == kIssuer && j.tiles > 0) {
+        constexpr uint32_t sdesc = kMmaDesc<kStep, false>, odesc = kMmaDesc<D, true>;
         const uint32_t one = elect_one();
         const uint64_t qd = matrix_desc(smem_addr(qs), 16, 1024), kd = matrix_desc(smem_addr(kbuf), 16, 1024);
         const uint64_t vd = matrix_desc(smem_addr(vbuf), KT * 128, 1024);
         // (start addresses count in 16 bytes)
-        auto scores = [&](int i, int mt, int sb) {
-          const uint64_t kt = kd + (i % ST) * (C::TILE / 16);
+        auto scores = [&](int i, int mt) {                  // step i's, into its buffer
+          const int tile = i / C::STEPS;
+          const uint64_t kt = kd + (tile % ST) * (C::TILE / 16) + (C::STEPS == 2 ? (i & 1) * (kStep * 128 / 16) : 0);
 #pragma unroll
           for (int k = 0; k < D / 16; ++k)
-            mma_ss(one, tmem + C::S0 + sb * C::SCOLS, qd + (mt * C::CB + k / 4) * (16384 / 16) + (k % 4) * 2,
+            mma_ss(one, tmem + (mt * 2 + (i & 1)) * kStep, qd + (mt * C::CB + k / 4) * (16384 / 16) + (k % 4) * 2,
                    kt + (k / 4) * (KT * 128 / 16) + (k % 4) * 2, sdesc, k > 0);
+          mma_commit(one, &s_full[mt * 2 + (i & 1)]);
+          if (mt == C::MT - 1 && (i + 1) % C::STEPS == 0) mma_commit(one, &k_empty[tile % ST]);
         };
-        auto values = [&](int i, int mt, int sb) {
-          const uint64_t vt = vd + (i % ST) * (C::TILE / 16);
+        auto values = [&](int i, int mt) {
+          const int tile = i / C::STEPS;
+          const uint64_t vt = vd + (tile % ST) * (C::TILE / 16) + (C::STEPS == 2 ? (i & 1) * (kStep * 128 / 16) : 0);
 #pragma unroll
-          for (int k = 0; k < KT / 16; ++k)
-            mma_ts(one, tmem + C::O0 + mt * D, tmem + C::S0 + sb * C::SCOLS + 8 * k, vt + k * (2048 / 16), odesc,
+          for (int k = 0; k < kStep / 16; ++k)
+            mma_ts(one, tmem + C::O0 + mt * D, tmem + (mt * 2 + (i & 1)) * kStep + 8 * k, vt + k * (2048 / 16), odesc,
                    i > 0 || k > 0);
+          mma_commit(one, &o_full[mt * 2 + (i & 1)]);
+          if (mt == C::MT - 1 && (i + 1) % C::STEPS == 0) mma_commit(one, &v_empty[tile % ST]);
         };
-        const int n = j.tiles;
-        if (wait(&k_full[0], 0)) {
+        // K and V tiles are waited for at their first steps
+        auto keys_in = [&](int i) {
+          const int tile = i / C::STEPS;
+          if (i % C::STEPS == 0) wait(&k_full[tile % ST], (tile / ST) & 1);
           tmem_fence_after();
-          scores(0, 0, 0);
-          mma_commit(one, &s_full[0]);
-          if constexpr (C::MT == 2) {
-            scores(0, 1, 1);
-            mma_commit(one, &s_full[1]);
-          }
-          mma_commit(one, &k_empty[0]);
+          return ok;
+        };
+        const int n = j.steps;
+#pragma unroll 1
+        for (int i = 0; i < 2 && i < n; ++i) {
+          if (!keys_in(i)) break;
+#pragma unroll
+          for (int mt = 0; mt < C::MT; ++mt) scores(i, mt);
         }
 #pragma unroll 1
         for (int i = 0; i < n && ok; ++i) {
-          const uint32_t vpar = (i / ST) & 1, kpar = ((i + 1) / ST) & 1;
-          if constexpr (C::MT == 2) {
-            if (!wait(&v_full[i % ST], vpar)) break;
+          const int tile = i / C::STEPS;
+          if (i % C::STEPS == 0 && !wait(&v_full[tile % ST], (tile / ST) & 1)) break;
 #pragma unroll
-            for (int mt = 0; mt < 2; ++mt) {
-              if (!wait(&p_full[mt], i & 1)) break;
-              tmem_fence_after();
-              values(i, mt, mt);
-              mma_commit(one, &o_full[mt]);
-              if (mt == 1) mma_commit(one, &v_empty[i % ST]);
-              if (i + 1 < n) {
-                if (mt == 0 && !wait(&k_full[(i + 1) % ST], kpar)) break;
-                tmem_fence_after();
-                scores(i + 1, mt, mt);
-                mma_commit(one, &s_full[mt]);
-                if (mt == 1) mma_commit(one, &k_empty[(i + 1) % ST]);
-              }
-            }
-          } else {
-            if (i + 1 < n) {
-              if (!wait(&k_full[(i + 1) % ST], kpar)) break;
-              tmem_fence_after();
-              scores(i + 1, 0, (i + 1) & 1);
-              mma_commit(one, &s_full[(i + 1) & 1]);
-              mma_commit(one, &k_empty[(i + 1) % ST]);
-            }
-            if (!wait(&v_full[i % ST], vpar) || !wait(&p_full[i & 1], (i >> 1) & 1)) break;
+          for (int mt = 0; mt < C::MT; ++mt) {
+            if (!wait(&p_full[mt * 2 + (i & 1)], (i >> 1) & 1)) break;
             tmem_fence_after();
-            values(i, 0, i & 1);
-            mma_commit(one, &o_full[0]);
-            mma_commit(one, &v_empty[i % ST]);
+            values(i, mt);
+            // the buffer is free once that product has read it, which is before
+            // the next one of this thread writes it
+            if (i + 2 < n) {
+              if (mt == 0 && !keys_in(i + 2)) break;
+              scores(i + 2, mt);
+            }
           }
         }
       }
-    } else {
+    }
+  } else {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" :: "n"(kConvertRegs));
+    {
       // ---- codes to fp16, the next tile's loads in flight over this one's
       // conversion and wait
       const bool is_v = warp >= kFirstV;
@@ -665,6 +645,10 @@ cudaError_t launch(const AttnArgs& a, int nsplit, cudaStream_t st) {
   if (dev >= 64 || ready[dev].load(std::memory_order_relaxed) == 0) {
     e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
     if (e != cudaSuccess) return e;
+    cudaFuncAttributes fa;
+    e = cudaFuncGetAttributes(&fa, k);
+    if (e != cudaSuccess) return e;
+    if (fa.numRegs * kThreads < kRegsNeeded) return cudaErrorInvalidKernelImage;
     if (dev < 64) ready[dev].store(1, std::memory_order_relaxed);
   }
   const int64_t tiles = (a.total_q * a.R / C::ROWS + a.c.B) * a.c.Hkv;
