@@ -255,22 +255,32 @@ int decode_grid(int B, int max_blocks, int Hq, int Hkv, int D, int block) {
 }
 int64_t decode_bytes(int grid, int D) { return static_cast<int64_t>(grid) * (2 * 8 * (D + 4) * 4 + 16); }
 
-// Tiles of a prompt call, and the splits of their keys: where the tiles leave
-// SMs idle, as many as fill them, each with at least two tiles of keys.
+// Tiles of a prompt call, and the splits of their keys.  A thread block has an
+// SM to itself; n splits take ceil(tiles n / SMs) rounds of a block's fixed
+// cost (about six key tiles' time) and an n-th of the keys, for which half the
+// table's room stands (causal, and tables are seldom full), or the window.
 struct PromptGrid {
   int64_t tiles;
   int nsplit;
   int64_t bytes;
 };
-PromptGrid prompt_grid(int B, int max_blocks, int64_t total_q, int Hq, int Hkv, int D, int block) {
+PromptGrid prompt_grid(int B, int max_blocks, int64_t total_q, int Hq, int Hkv, int D, int block, int window) {
   const int rows = D == 256 ? 128 : 256, kt = D == 256 ? 64 : 128;
   PromptGrid g;
   g.tiles = (total_q * (Hq / Hkv) / rows + B) * Hkv;
-  const int64_t most = static_cast<int64_t>(max_blocks) * block / kt / 2;
-  int64_t n = g.tiles > 0 ? sm_count() / g.tiles : 1;
-  n = n > most ? most : n;
-  n = n > 32 ? 32 : n;
-  g.nsplit = n > 1 ? static_cast<int>(n) : 1;
+  int64_t keys = static_cast<int64_t>(max_blocks) * block / kt / 2;
+  const int64_t seen = (static_cast<int64_t>(window) + rows * Hkv / Hq) / kt + 1, sms = sm_count();
+  if (window > 0 && seen < keys) keys = seen;
+  g.nsplit = 1;
+  int64_t best = (g.tiles + sms - 1) / sms * (6 + keys) * 16;
+  for (int n = 2; n <= 16 && n <= keys / 2 && g.tiles < 2 * sms; ++n) {
+    // a sixteenth more must be gained by each further split's partial sums
+    const int64_t cost = (g.tiles * n + sms - 1) / sms * (6 + (keys + n - 1) / n) * 17;
+    if (cost < best) {
+      best = cost;
+      g.nsplit = n;
+    }
+  }
   g.bytes = g.nsplit > 1 ? g.tiles * g.nsplit * rows * (D + 4) * 4 : 0;
   return g;
 }
@@ -430,7 +440,7 @@ int64_t kvq_paged_workspace_bytes(int B, int max_blocks, int64_t total_q, int Hq
   if (check_shape(KVQ_FP16, KVQ_INT8, B, max_blocks, Hkv, D, block, 0) != KVQ_OK) return -1;
   if (Hq < Hkv || Hq % Hkv != 0 || total_q < 0 || total_q > INT32_MAX || total_q * Hq > INT32_MAX) return -1;
   const int64_t one = decode_bytes(decode_grid(B, max_blocks, Hq, Hkv, D, block), D);
-  const int64_t many = prompt_grid(B, max_blocks, total_q, Hq, Hkv, D, block).bytes;
+  const int64_t many = prompt_grid(B, max_blocks, total_q, Hq, Hkv, D, block, 0).bytes;
   return one > many ? one : many;
 }
 
@@ -465,7 +475,7 @@ int kvq_paged_attention_prefill(const void* q, int dtype, int64_t q_stride, cons
                                 block, format, num_blocks, k_codes, v_codes, k_scales, v_scales, sm_scale, window, out);
   if (rc != KVQ_OK || p.q == nullptr) return rc;
   if (!cu_q) return KVQ_ERR_NULL;
-  PromptGrid g = prompt_grid(B, max_blocks, total_q, Hq, Hkv, D, block);
+  PromptGrid g = prompt_grid(B, max_blocks, total_q, Hq, Hkv, D, block, window);
   if (g.tiles * (D == 256 ? 16 : 32) > INT32_MAX) return KVQ_ERR_COUNT;
   if (g.nsplit > 1 && workspace && aligned_to(workspace, 16) && workspace_bytes >= g.bytes)
     p.part = static_cast<float*>(workspace);

@@ -34,6 +34,7 @@
 
 #include <atomic>
 #include <cstdint>
+#include <type_traits>
 
 #include "kvq.h"
 #include "kvq_paged_attn.cuh"
@@ -103,6 +104,22 @@ __device__ __forceinline__ void tmem_st32(uint32_t addr, const uint32_t (&r)[32]
          "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]),
          "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]),
          "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31]), "r"(addr)
+      : "memory");
+}
+
+// And 16 columns.
+__device__ __forceinline__ void tmem_ld16(uint32_t (&r)[16], uint32_t addr) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(addr));
+}
+__device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15};"
+      :: "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
+         "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(addr)
       : "memory");
 }
 
@@ -262,7 +279,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_prefill_kernel(AttnArgs a, 
   uint64_t *meta_full = bars + 4 * ST, *s_full = meta_full + 4, *p_full = s_full + 4, *o_full = p_full + 4;
   uint32_t* shared_word = reinterpret_cast<uint32_t*>(bars + C::NBAR);         // the tensor memory's address
 
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(kAll, tid >> 5, 0);
   unsigned bad = 0;
   Job j;
   if (!find_job<D>(a, nsplit, j, bad)) {
@@ -287,56 +304,56 @@ __global__ void __launch_bounds__(kThreads, 1) paged_prefill_kernel(AttnArgs a, 
     mbar_fence_init();
   }
 
-  // ---- the query rows, fp16 with a power of two each, channels in code order
-  for (int r = warp; r < C::ROWS; r += kThreads / 32) {
-    constexpr int PER = D / 128 > 0 ? D / 128 : 1;          // 4-channel groups a lane
-    uint2 w[PER];
-    const bool live = r < j.count;
-    const int row = j.row0 + r, tok = row / a.R;
-    const uint16_t* q = a.q + (j.q0 + static_cast<int64_t>(tok)) * a.q_stride +
-                        static_cast<int64_t>(j.kvh * a.R + row % a.R) * D;
+  // ---- the query rows, fp16 with a power of two each, channels in code order:
+  // a lane has 8 channels, a row D / 8 lanes, and all loads of a warp are in
+  // flight before the first is used
+  {
+    constexpr int LANES = D / 8, AT_ONCE = 32 / LANES, W = kThreads / 32 * AT_ONCE, N = (C::ROWS + W - 1) / W;
+    const int c = lane % LANES;
+    uint4 w[N];
 #pragma unroll
-    for (int i = 0; i < PER; ++i) {
-      const int g = i * 32 + lane;
-      w[i] = live && g < D / 4 ? *reinterpret_cast<const uint2*>(q + 4 * g) : make_uint2(0, 0);
+    for (int n = 0; n < N; ++n) {
+      const int r = n * W + warp * AT_ONCE + lane / LANES, row = j.row0 + r, tok = row / a.R;
+      const uint16_t* q = a.q + (j.q0 + static_cast<int64_t>(tok)) * a.q_stride +
+                          static_cast<int64_t>(j.kvh * a.R + row - tok * a.R) * D + c * 8;
+      w[n] = r < j.count ? __ldg(reinterpret_cast<const uint4*>(q)) : make_uint4(0, 0, 0, 0);
     }
-    float u = a.scale * kCodeUnit<FMT>;
-    if (a.bf16) {
-      float most = 0.0f;
 #pragma unroll
-      for (int i = 0; i < PER; ++i) {
-        const float2 x = unpack2<true>(w[i].x), y = unpack2<true>(w[i].y);
-        most = fmaxf(most, fmaxf(fmaxf(fabsf(x.x), fabsf(x.y)), fmaxf(fabsf(y.x), fabsf(y.y))));
+    for (int n = 0; n < N; ++n) {
+      const int r = n * W + warp * AT_ONCE + lane / LANES;
+      float u = a.scale * kCodeUnit<FMT>;
+      uint32_t h[4] = {w[n].x, w[n].y, w[n].z, w[n].w};
+      if (a.bf16) {
+        float2 x[4];
+        float most = 0.0f;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          x[i] = unpack2<true>(h[i]);
+          most = max3(most, fabsf(x[i].x), fabsf(x[i].y));
+        }
+#pragma unroll
+        for (int o = LANES / 2; o > 0; o >>= 1) most = fmaxf(most, __shfl_xor_sync(kAll, most, o));
+        const int k = row_exponent(most);
+        const float up = pow2i(k);
+        u *= pow2i(-k);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) h[i] = pack2<false>(x[i].x * up, x[i].y * up);
       }
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) most = fmaxf(most, __shfl_xor_sync(kAll, most, o));
-      const int k = row_exponent(most);
-      const float up = pow2i(k);
-      u *= pow2i(-k);
-#pragma unroll
-      for (int i = 0; i < PER; ++i) {
-        const float2 x = unpack2<true>(w[i].x), y = unpack2<true>(w[i].y);
-        w[i].x = pack2<false>(x.x * up, x.y * up);
-        w[i].y = pack2<false>(y.x * up, y.y * up);
+      const uint32_t sign = a.negative ? 0x80008000u : 0u;
+      if (r < C::ROWS) {
+        const int rr = r & 127;
+        *reinterpret_cast<uint4*>(qs + ((r >> 7) * C::CB + (c >> 3)) * 16384 + rr * 128 + (((c & 7) ^ (rr & 7)) << 4)) =
+            make_uint4(__byte_perm(h[0], h[1], 0x5410) ^ sign, __byte_perm(h[0], h[1], 0x7632) ^ sign,
+                       __byte_perm(h[2], h[3], 0x5410) ^ sign, __byte_perm(h[2], h[3], 0x7632) ^ sign);
+        if (c == 0) unit[r] = u;
       }
     }
-    const uint32_t sign = a.negative ? 0x80008000u : 0u;
-#pragma unroll
-    for (int i = 0; i < PER; ++i) {
-      const int g = i * 32 + lane;                          // channels 4 g .. 4 g + 3
-      if (g < D / 4) {
-        const uint2 h = make_uint2(__byte_perm(w[i].x, w[i].y, 0x5410) ^ sign, __byte_perm(w[i].x, w[i].y, 0x7632) ^ sign);
-        const int rr = r & 127, cb = g >> 4, un = (g & 15) >> 1;
-        *reinterpret_cast<uint2*>(qs + ((r >> 7) * C::CB + cb) * 16384 + rr * 128 + ((un ^ (rr & 7)) << 4) + (g & 1) * 8) = h;
-      }
-    }
-    if (lane == 0) unit[r] = u;
   }
   fence_proxy_async();
   tmem_fence_before();
   __syncthreads();
   tmem_fence_after();
-  const uint32_t tmem = *shared_word;
+  const uint32_t tmem = __shfl_sync(kAll, *shared_word, 0);
   bool ok = true;                                 // this role has met no timeout
   auto wait = [&](uint64_t* bar, uint32_t parity) {         // a whole warp, of one mind
     if (ok) ok = __all_sync(kAll, mbar_wait(bar, parity, kSpin));
@@ -370,66 +387,72 @@ __global__ void __launch_bounds__(kThreads, 1) paged_prefill_kernel(AttnArgs a, 
         const uint32_t s_at = lanes + buf * kStep;
         if (!wait(&s_full[buf], (i >> 1) & 1) || !wait(&meta_full[tile & 3], (tile >> 2) & 1)) break;
         tmem_fence_after();
-        uint32_t s[2][32];
-        tmem_ld32(s[0], s_at);
-        tmem_ld32(s[1], s_at + 32);
-        tmem_wait_ld();
         const float4* sc = meta + (tile & 3) * NSUB + (C::STEPS == 2 ? (i & 1) * 4 : 0);
         const int key0 = j.first + i * kStep;
-        if (key0 + kStep - 1 > wpos || key0 < wlow) {
-          const int up = pos - key0, down = low - key0;     // columns down .. up are seen
+        auto step = [&](auto edge) -> bool {
+          uint32_t s[2][32], w[kStep / 2];
+          tmem_ld32(s[0], s_at);
+          tmem_ld32(s[1], s_at + 32);
+          tmem_wait_ld();
+          if constexpr (decltype(edge)::value) {
+            const int up = pos - key0, down = low - key0;   // columns down .. up are seen
 #pragma unroll
-          for (int c = 0; c < kStep; ++c)
-            if (c > up || c < down) s[c / 32][c % 32] = 0xff800000u;       // -inf
-        }
-        auto at = [&](int c) { return __uint_as_float(s[c / 32][c % 32]); };
-        float most = -INFINITY;
+            for (int c = 0; c < kStep; ++c)
+              if (c > up || c < down) s[c / 32][c % 32] = 0xff800000u;     // -inf
+          }
+          auto at = [&](int c) { return __uint_as_float(s[c / 32][c % 32]); };
+          float most = -INFINITY, ak[kStep / 16], bk[kStep / 16], vk[kStep / 16];
 #pragma unroll
-        for (int k = 0; k < kStep / 16; ++k) {
-          float x = fmaxf(at(16 * k), at(16 * k + 15));
+          for (int k = 0; k < kStep / 16; ++k) {
+            float x = fmaxf(at(16 * k), at(16 * k + 15));
 #pragma unroll
-          for (int e = 1; e < 15; e += 2) x = max3(x, at(16 * k + e), at(16 * k + e + 1));
-          const float4 m4 = sc[k];
-          most = fmaxf(most, fmaf(x, fmaxf(u * m4.x, 1e-30f), m4.y));
-        }
-        if (__any_sync(kAll, most > M + kLazy)) {
-          const float now = fmaxf(M, most);
-          const float f = now == -INFINITY ? 1.0f : exp2_approx(M - now);
-          M = now;
-          l *= f;
-          if (i > 0) {                                      // O so far, after its last product
-            if (!wait(&o_full[mt * 2 + ((i - 1) & 1)], ((i - 1) >> 1) & 1)) break;
-            tmem_fence_after();
+            for (int e = 1; e < 15; e += 2) x = max3(x, at(16 * k + e), at(16 * k + e + 1));
+            const float4 m4 = sc[k];
+            ak[k] = fmaxf(u * m4.x, 1e-30f);                // never 0, which would make NaN of -inf
+            bk[k] = m4.y;
+            vk[k] = m4.z;
+            most = fmaxf(most, fmaf(x, ak[k], bk[k]));
+          }
+          if (__any_sync(kAll, most > M + kLazy)) {
+            const float now = fmaxf(M, most);
+            const float f = now == -INFINITY ? 1.0f : exp2_approx(M - now);
+            M = now;
+            l *= f;
+            if (i > 0) {                                      // O so far, after its last product
+              if (!wait(&o_full[mt * 2 + ((i - 1) & 1)], ((i - 1) >> 1) & 1)) return false;
+              tmem_fence_after();
 #pragma unroll 1
-            for (int c = 0; c < D / 32; ++c) {
-              uint32_t o[32];
-              tmem_ld32(o, o_at + 32 * c);
-              tmem_wait_ld();
+              for (int c = 0; c < D / 16; ++c) {
+                uint32_t o[16];
+                tmem_ld16(o, o_at + 16 * c);
+                tmem_wait_ld();
 #pragma unroll
-              for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
-              tmem_st32(o_at + 32 * c, o);
+                for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+                tmem_st16(o_at + 16 * c, o);
+              }
             }
           }
-        }
-        const float ref = M == -INFINITY ? 0.0f : kBoost - M;
-        uint32_t w[32];
+          const float ref = M == -INFINITY ? 0.0f : kBoost - M;
 #pragma unroll
-        for (int k = 0; k < kStep / 16; ++k) {
-          const float4 m4 = sc[k];
-          const float ak = fmaxf(u * m4.x, 1e-30f), ck = m4.y + ref;
-          const float2 a2 = make_float2(ak, ak), c2 = make_float2(ck, ck);
-          float2 sum = make_float2(0.0f, 0.0f);
+          for (int k = 0; k < kStep / 16; ++k) {
+            const float ck = bk[k] + ref;
+            const float2 a2 = make_float2(ak[k], ak[k]), c2 = make_float2(ck, ck);
+            float2 sum = make_float2(0.0f, 0.0f);
 #pragma unroll
-          for (int e = 0; e < 16; e += 2) {
-            float2 p = __ffma2_rn(make_float2(at(16 * k + e), at(16 * k + e + 1)), a2, c2);
-            p.x = exp2_approx(p.x);
-            p.y = exp2_approx(p.y);
-            sum = __fadd2_rn(sum, p);
-            w[8 * k + e / 2] = pack2<false>(p.x, p.y);
+            for (int e = 0; e < 16; e += 2) {
+              float2 p = __ffma2_rn(make_float2(at(16 * k + e), at(16 * k + e + 1)), a2, c2);
+              p.x = exp2_approx(p.x);
+              p.y = exp2_approx(p.y);
+              sum = __fadd2_rn(sum, p);
+              w[8 * k + e / 2] = pack2<false>(p.x, p.y);
+            }
+            l = fmaf(sum.x + sum.y, vk[k], l);
           }
-          l = fmaf(sum.x + sum.y, m4.z, l);
-        }
-        tmem_st32(s_at, w);
+          tmem_st32(s_at, w);
+          return true;
+        };
+        const bool edge = key0 + kStep - 1 > wpos || key0 < wlow;
+        if (!(edge ? step(std::true_type{}) : step(std::false_type{}))) break;
         tmem_wait_st();
         tmem_fence_before();
         __syncwarp();
@@ -439,11 +462,8 @@ __global__ void __launch_bounds__(kThreads, 1) paged_prefill_kernel(AttnArgs a, 
       if (j.steps > 0 && wait(&o_full[mt * 2 + ((j.steps - 1) & 1)], ((j.steps - 1) >> 1) & 1)) tmem_fence_after();
       const bool some = j.steps > 0 && ok;
       const float inv = l == 0.0f ? 0.0f : kCodeUnit<FMT> / l;
-      const int64_t token = j.q0 + static_cast<int64_t>(live ? row / a.R : 0);
-      uint16_t* out = a.out + (token * a.c.Hkv * a.R + j.kvh * a.R + (live ? row % a.R : 0)) * D;
-      float* part = nullptr;
-      if (nsplit > 1) part = a.part + ((j.tile * nsplit + j.split) * C::ROWS + r) * (D + 4);
-      if (ok) {
+      if (ok && nsplit > 1) {
+        float* part = a.part + ((j.tile * nsplit + j.split) * C::ROWS + r) * (D + 4);
 #pragma unroll 1
         for (int c = 0; c < D / 32; ++c) {
           uint32_t o[32];
@@ -454,26 +474,53 @@ __global__ void __launch_bounds__(kThreads, 1) paged_prefill_kernel(AttnArgs a, 
 #pragma unroll
             for (int e = 0; e < 32; ++e) o[e] = 0;
           }
-          if (live && nsplit == 1) {
-#pragma unroll
-            for (int e = 0; e < 32; e += 8) {
-              uint32_t h[4];
-#pragma unroll
-              for (int k = 0; k < 2; ++k) {                 // columns hold channels 0, 2, 1, 3 of each four
-                const float x0 = __uint_as_float(o[e + 4 * k]) * inv, x2 = __uint_as_float(o[e + 4 * k + 1]) * inv;
-                const float x1 = __uint_as_float(o[e + 4 * k + 2]) * inv, x3 = __uint_as_float(o[e + 4 * k + 3]) * inv;
-                h[2 * k] = a.bf16 ? pack2<true>(x0, x1) : pack2<false>(x0, x1);
-                h[2 * k + 1] = a.bf16 ? pack2<true>(x2, x3) : pack2<false>(x2, x3);
-              }
-              *reinterpret_cast<uint4*>(out + 32 * c + e) = make_uint4(h[0], h[1], h[2], h[3]);
-            }
-          } else if (live) {
+          if (live) {                                       // columns hold channels 0, 2, 1, 3 of each four
 #pragma unroll
             for (int e = 0; e < 32; e += 4)
               *reinterpret_cast<uint4*>(part + 32 * c + e) = make_uint4(o[e], o[e + 2], o[e + 1], o[e + 3]);
           }
         }
-        if (live && nsplit > 1) *reinterpret_cast<float2*>(part + D) = make_float2(M, l);
+        if (live) *reinterpret_cast<float2*>(part + D) = make_float2(M, l);
+      } else if (ok) {
+        // through shared memory, where the queries are no longer needed, so that
+        // rows go out whole: this warp's 32 rows, 16-byte unit c at c ^ (row mod 8)
+        uint8_t* mine = qs + (mt * 128 + (warp & 3) * 32) * D * 2;
+#pragma unroll 1
+        for (int c = 0; c < D / 32; ++c) {
+          uint32_t o[32];
+          if (some) {
+            tmem_ld32(o, o_at + 32 * c);
+            tmem_wait_ld();
+          } else {
+#pragma unroll
+            for (int e = 0; e < 32; ++e) o[e] = 0;
+          }
+#pragma unroll
+          for (int e = 0; e < 32; e += 8) {
+            uint32_t h[4];
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+              const float x0 = __uint_as_float(o[e + 4 * k]) * inv, x2 = __uint_as_float(o[e + 4 * k + 1]) * inv;
+              const float x1 = __uint_as_float(o[e + 4 * k + 2]) * inv, x3 = __uint_as_float(o[e + 4 * k + 3]) * inv;
+              h[2 * k] = a.bf16 ? pack2<true>(x0, x1) : pack2<false>(x0, x1);
+              h[2 * k + 1] = a.bf16 ? pack2<true>(x2, x3) : pack2<false>(x2, x3);
+            }
+            const int un = 4 * c + e / 8;
+            *reinterpret_cast<uint4*>(mine + lane * D * 2 + ((un ^ (lane & 7)) << 4)) = make_uint4(h[0], h[1], h[2], h[3]);
+          }
+        }
+        __syncwarp();
+        constexpr int UNITS = D / 8, AT_ONCE = 32 / UNITS;  // units of a row, rows of one store
+        const int un = lane % UNITS;
+        const int64_t tok = row / a.R, head = row % a.R;    // each lane finds its row's place
+        const int64_t place = live ? ((j.q0 + tok) * a.c.Hkv * a.R + j.kvh * a.R + head) * D : -1;
+#pragma unroll 4
+        for (int k = 0; k < 32 / AT_ONCE; ++k) {
+          const int x = k * AT_ONCE + lane / UNITS;
+          const int64_t to = __shfl_sync(kAll, place, x);
+          const uint4 v = *reinterpret_cast<const uint4*>(mine + x * D * 2 + ((un ^ (x & 7)) << 4));
+          if (to >= 0) *reinterpret_cast<uint4*>(a.out + to + un * 8) = v;
+        }
       }
       tmem_fence_before();
     }
@@ -514,7 +561,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_prefill_kernel(AttnArgs a, 
           tmem_fence_after();
           return ok;
         };
-        const int n = j.steps;
+        const int n = __shfl_sync(kAll, j.steps, 0);
 #pragma unroll 1
         for (int i = 0; i < 2 && i < n; ++i) {
           if (!keys_in(i)) break;
