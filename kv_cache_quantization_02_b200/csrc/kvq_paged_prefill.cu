@@ -295,7 +295,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_prefill_kernel(AttnArgs a, 
   if (tid == 0) {
     for (int i = 0; i < ST; ++i) {
       mbar_init(&k_full[i], 4); mbar_init(&v_full[i], 4);
-      mbar_init(&k_empty[i], 1); mbar_init(&v_empty[i], 1);
+      mbar_init(&k_empty[i], C::MT); mbar_init(&v_empty[i], C::MT);
     }
     for (int i = 0; i < 4; ++i) mbar_init(&meta_full[i], 1);
     // per 128 rows, steps alternate between two of each: a wait is then never two
@@ -528,13 +528,14 @@ __global__ void __launch_bounds__(kThreads, 1) paged_prefill_kernel(AttnArgs a, 
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" :: "n"(kIssuerRegs));
     {
       // ---- the MMAs
-      if (warp == kIssuer && j.tiles > 0) {
+      if (warp < kIssuer + C::MT && j.tiles > 0) {
+        const int mt = warp - kIssuer;
         constexpr uint32_t sdesc = kMmaDesc<kStep, false>, odesc = kMmaDesc<D, true>;
         const uint32_t one = elect_one();
         const uint64_t qd = matrix_desc(smem_addr(qs), 16, 1024), kd = matrix_desc(smem_addr(kbuf), 16, 1024);
         const uint64_t vd = matrix_desc(smem_addr(vbuf), KT * 128, 1024);
         // (start addresses count in 16 bytes)
-        auto scores = [&](int i, int mt) {                  // step i's, into its buffer
+        auto scores = [&](int i) {                  // step i's, into its buffer
           const int tile = i / C::STEPS;
           const uint64_t kt = kd + (tile % ST) * (C::TILE / 16) + (C::STEPS == 2 ? (i & 1) * (kStep * 128 / 16) : 0);
 #pragma unroll
@@ -542,9 +543,9 @@ __global__ void __launch_bounds__(kThreads, 1) paged_prefill_kernel(AttnArgs a, 
             mma_ss(one, tmem + (mt * 2 + (i & 1)) * kStep, qd + (mt * C::CB + k / 4) * (16384 / 16) + (k % 4) * 2,
                    kt + (k / 4) * (KT * 128 / 16) + (k % 4) * 2, sdesc, k > 0);
           mma_commit(one, &s_full[mt * 2 + (i & 1)]);
-          if (mt == C::MT - 1 && (i + 1) % C::STEPS == 0) mma_commit(one, &k_empty[tile % ST]);
+          if ((i + 1) % C::STEPS == 0) mma_commit(one, &k_empty[tile % ST]);
         };
-        auto values = [&](int i, int mt) {
+        auto values = [&](int i) {
           const int tile = i / C::STEPS;
           const uint64_t vt = vd + (tile % ST) * (C::TILE / 16) + (C::STEPS == 2 ? (i & 1) * (kStep * 128 / 16) : 0);
 #pragma unroll
@@ -552,7 +553,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_prefill_kernel(AttnArgs a, 
             mma_ts(one, tmem + C::O0 + mt * D, tmem + (mt * 2 + (i & 1)) * kStep + 8 * k, vt + k * (2048 / 16), odesc,
                    i > 0 || k > 0);
           mma_commit(one, &o_full[mt * 2 + (i & 1)]);
-          if (mt == C::MT - 1 && (i + 1) % C::STEPS == 0) mma_commit(one, &v_empty[tile % ST]);
+          if ((i + 1) % C::STEPS == 0) mma_commit(one, &v_empty[tile % ST]);
         };
         // K and V tiles are waited for at their first steps
         auto keys_in = [&](int i) {
@@ -565,24 +566,20 @@ __global__ void __launch_bounds__(kThreads, 1) paged_prefill_kernel(AttnArgs a, 
 #pragma unroll 1
         for (int i = 0; i < 2 && i < n; ++i) {
           if (!keys_in(i)) break;
-#pragma unroll
-          for (int mt = 0; mt < C::MT; ++mt) scores(i, mt);
+          scores(i);
         }
 #pragma unroll 1
         for (int i = 0; i < n && ok; ++i) {
           const int tile = i / C::STEPS;
           if (i % C::STEPS == 0 && !wait(&v_full[tile % ST], (tile / ST) & 1)) break;
-#pragma unroll
-          for (int mt = 0; mt < C::MT; ++mt) {
-            if (!wait(&p_full[mt * 2 + (i & 1)], (i >> 1) & 1)) break;
-            tmem_fence_after();
-            values(i, mt);
-            // the buffer is free once that product has read it, which is before
-            // the next one of this thread writes it
-            if (i + 2 < n) {
-              if (mt == 0 && !keys_in(i + 2)) break;
-              scores(i + 2, mt);
-            }
+          if (!wait(&p_full[mt * 2 + (i & 1)], (i >> 1) & 1)) break;
+          tmem_fence_after();
+          values(i);
+          // the buffer is free once that product has read it, which is before
+          // the next one of this thread writes it
+          if (i + 2 < n) {
+            if (!keys_in(i + 2)) break;
+            scores(i + 2);
           }
         }
       }
