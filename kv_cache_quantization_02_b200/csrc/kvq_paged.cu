@@ -27,10 +27,11 @@ struct Tokens {
   int64_t n_tokens;
 };
 
-// What one thread block works on: the tokens of one sequence that fall into
-// one cache block, of one KV head, in K or V.
+// What one thread block, or one warp, works on: the tokens of one sequence that
+// fall into one cache block, of one KV head, in K or V.
 struct Item {
-  int id;                 // cache block, or -1: nothing to do
+  int b;                  // sequence
+  int64_t blk;            // the sequence's block, -1: nothing to do
   int head;
   bool is_v;
   int slot;               // the first token's slot
@@ -41,40 +42,52 @@ struct Item {
 // Item numbers run over (sequence, block of its new tokens, head, K or V), the
 // last fastest: neighbouring thread blocks read neighbouring pieces of the
 // same token rows.  A sequence of n tokens touches at most floor(n / block) + 2
-// blocks.
-__device__ __forceinline__ Item find_item(const Cache& c, const Tokens& t, unsigned& bad) {
+// blocks.  A warp finds its item; the table is read apart from that, so that
+// the new tokens' loads need not wait for it.
+__device__ __forceinline__ Item find_item(const Cache& c, const Tokens& t, unsigned x, int lane) {
+  unsigned bad = 0;
+  Item it;
+  it.blk = -1;
+  it.slot = it.count = 0;
+  it.row = 0;
+  it.is_v = x & 1;
+  x >>= 1;
+  it.head = static_cast<int>(x % c.Hkv);
+  const Found f = find_sequence(t.cu, t.start, c.B, x / c.Hkv, 1, c.log_block, 2, lane);
+  const int64_t c0 = f.c0, c1 = f.c1, p0 = f.more;
+  it.b = f.b;
+  if (c0 < 0 || c1 < c0 || c1 > t.n_tokens || (p0 < 0 && c1 > c0)) {
+    bad |= kFaultLength;
+  } else if (c1 > c0 && f.item >= 0) {
+    const int64_t blk = (p0 >> c.log_block) + f.item;
+    const int64_t lo = max(p0, blk << c.log_block), hi = min(p0 + (c1 - c0), (blk + 1) << c.log_block);
+    if (lo < hi) {
+      it.blk = blk;
+      it.slot = static_cast<int>(lo & (c.block - 1));
+      it.count = static_cast<int>(hi - lo);
+      it.row = c0 + (lo - p0);
+    }
+  }
+  if (lane == 0) report(bad);
+  return it;
+}
+// A thread block's item, found by its first warp.
+__device__ __forceinline__ Item find_block_item(const Cache& c, const Tokens& t) {
   __shared__ Item item;
   if (threadIdx.x < 32) {
-    const int lane = threadIdx.x;
-    int64_t x = blockIdx.x;
-    Item it;
-    it.id = -1;
-    it.is_v = x & 1;
-    x >>= 1;
-    it.head = static_cast<int>(x % c.Hkv);
-    x /= c.Hkv;
-    const int b = find_sequence(t.cu, c.B, x, 1, c.block, 2, lane);
-    const int64_t j = x - item_base(t.cu, b, 1, c.block, 2);
-    const int64_t c0 = t.cu[b], c1 = t.cu[b + 1], p0 = t.start[b];
-    if (c0 < 0 || c1 < c0 || c1 > t.n_tokens || (p0 < 0 && c1 > c0)) {
-      bad |= kFaultLength;
-    } else if (c1 > c0 && j >= 0) {
-      const int64_t blk = (p0 >> c.log_block) + j;
-      const int64_t lo = max(p0, blk << c.log_block), hi = min(p0 + (c1 - c0), (blk + 1) << c.log_block);
-      if (lo < hi) {
-        it.id = block_at(c, b, blk, bad);
-        it.slot = static_cast<int>(lo & (c.block - 1));
-        it.count = static_cast<int>(hi - lo);
-        it.row = c0 + (lo - p0);
-      }
-    }
-    if (lane == 0) {
-      item = it;
-      report(bad);
-    }
+    const Item it = find_item(c, t, blockIdx.x, threadIdx.x);
+    if (threadIdx.x == 0) item = it;
   }
   __syncthreads();
   return item;
+}
+
+// Its cache block, or -1.
+__device__ __forceinline__ int find_block(const Cache& c, const Item& it, int lane) {
+  unsigned bad = 0;
+  const int id = block_at(c, it.b, it.blk, bad);
+  if (lane == 0) report(bad);
+  return id;
 }
 
 // ---------------------------------------------------------------------------
@@ -85,22 +98,29 @@ __device__ __forceinline__ Item find_item(const Cache& c, const Tokens& t, unsig
 // slots are rounded again; the arithmetic is the header's, one IEEE operation
 // at a time.
 // ---------------------------------------------------------------------------
+template <int FMT>
+__device__ __forceinline__ uint4 recode16(uint4 w, float f) {
+  const uint32_t in[4] = {w.x, w.y, w.z, w.w};
+  uint32_t q[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    float y[4];
+    decode4<FMT>(in[e], y);
+    q[e] = encode4<FMT>(y[0] * f, y[1] * f, y[2] * f, y[3] * f);
+  }
+  return make_uint4(q[0], q[1], q[2], q[3]);
+}
 template <int FMT, bool BF16, int T, int VPT>
 __global__ void __launch_bounds__(T) paged_write_kernel(Cache c, Tokens t, const uint16_t* __restrict__ k,
                                                         const uint16_t* __restrict__ v, int64_t k_stride,
                                                         int64_t v_stride) {
-  unsigned bad = 0;
-  const Item it = find_item(c, t, bad);
-  if (it.id < 0) return;
+  const Item it = find_block_item(c, t);
+  if (it.blk < 0) return;
   const uint16_t* x = (it.is_v ? v : k) + it.row * (it.is_v ? v_stride : k_stride) + static_cast<int64_t>(it.head) * c.D;
   const int64_t stride = it.is_v ? v_stride : k_stride;
-  const int64_t bh = static_cast<int64_t>(it.id) * c.Hkv + it.head;
-  float* scale = (it.is_v ? c.vs : c.ks) + bh;
-  uint8_t* codes = (it.is_v ? c.vc : c.kc) + bh * c.block * c.D;
   const int upr = c.D >> 4;                       // units of a row, a power of two
   const int lu = 31 - __clz(upr);
   const int units = it.count << lu;
-  const float old = it.slot > 0 ? *scale : 0.0f;  // read by all before thread 0 writes it
 
   uint4 r[VPT][2];
   float a = 0.0f;
@@ -115,6 +135,12 @@ __global__ void __launch_bounds__(T) paged_write_kernel(Cache c, Tokens t, const
       r[i][0] = r[i][1] = make_uint4(0, 0, 0, 0);
     }
   }
+  const int id = find_block(c, it, threadIdx.x & 31);
+  if (id < 0) return;                             // all of the thread block
+  const int64_t bh = static_cast<int64_t>(id) * c.Hkv + it.head;
+  float* scale = (it.is_v ? c.vs : c.ks) + bh;
+  uint8_t* codes = (it.is_v ? c.vc : c.kc) + bh * c.block * c.D;
+  const float old = it.slot > 0 ? *scale : 0.0f;  // read by all before thread 0 writes it
 #pragma unroll
   for (int i = 0; i < VPT; ++i)
 #pragma unroll
@@ -160,19 +186,74 @@ __global__ void __launch_bounds__(T) paged_write_kernel(Cache c, Tokens t, const
   }
   if (it.slot > 0 && S > old) {
     const float f = __fdiv_rn(old, S);
-    for (int u = threadIdx.x; u < (it.slot << lu); u += T) {
-      uint4* p = reinterpret_cast<uint4*>(codes) + u;
-      const uint4 w = *p;
-      const uint32_t in[4] = {w.x, w.y, w.z, w.w};
-      uint32_t q[4];
+    uint4* p = reinterpret_cast<uint4*>(codes);
+    for (int u = threadIdx.x; u < (it.slot << lu); u += T) p[u] = recode16<FMT>(p[u], f);
+  }
+}
+
+// The same with a warp per item, for calls of about a token per sequence: four
+// times fewer thread blocks, and no barrier.  The first 32 units stay in
+// registers (two tokens at D = 256), any others are read again.
+template <int FMT, bool BF16>
+__device__ __forceinline__ float largest(uint4 w) {
+  const uint32_t v[4] = {w.x, w.y, w.z, w.w};
+  float a = 0.0f;
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        float y[4];
-        decode4<FMT>(in[e], y);
-        q[e] = encode4<FMT>(y[0] * f, y[1] * f, y[2] * f, y[3] * f);
-      }
-      *p = make_uint4(q[0], q[1], q[2], q[3]);
-    }
+  for (int e = 0; e < 4; ++e) {
+    const float2 f = unpack2<BF16>(v[e]);
+    a = fmaxf(a, fmaxf(fabsf(f.x), fabsf(f.y)));
+  }
+  return a;
+}
+template <int FMT, bool BF16>
+__device__ __forceinline__ uint4 encode16(uint4 lo, uint4 hi, float inv) {
+  const uint32_t w[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+  uint32_t q[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const float2 f = unpack2<BF16>(w[2 * e]), g = unpack2<BF16>(w[2 * e + 1]);
+    q[e] = encode4<FMT>(f.x * inv, f.y * inv, g.x * inv, g.y * inv);
+  }
+  return make_uint4(q[0], q[1], q[2], q[3]);
+}
+template <int FMT, bool BF16>
+__global__ void __launch_bounds__(128) paged_append_kernel(Cache c, Tokens t, int64_t items, const uint16_t* __restrict__ k,
+                                                           const uint16_t* __restrict__ v, int64_t k_stride,
+                                                           int64_t v_stride) {
+  const int lane = threadIdx.x & 31;
+  const int64_t number = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 5);
+  if (number >= items) return;
+  const Item it = find_item(c, t, static_cast<unsigned>(number), lane);
+  if (it.blk < 0) return;
+  const int64_t stride = it.is_v ? v_stride : k_stride;
+  const uint16_t* x = (it.is_v ? v : k) + it.row * stride + static_cast<int64_t>(it.head) * c.D;
+  const int upr = c.D >> 4, lu = 31 - __clz(upr), units = it.count << lu;
+  auto unit_at = [&](int u) { return reinterpret_cast<const uint4*>(x + (u >> lu) * stride + ((u & (upr - 1)) << 4)); };
+  uint4 r0 = make_uint4(0, 0, 0, 0), r1 = r0;
+  if (lane < units) { r0 = unit_at(lane)[0]; r1 = unit_at(lane)[1]; }
+  const int id = find_block(c, it, lane);
+  if (id < 0) return;
+  const int64_t bh = static_cast<int64_t>(id) * c.Hkv + it.head;
+  float* scale = (it.is_v ? c.vs : c.ks) + bh;
+  uint4* codes = reinterpret_cast<uint4*>((it.is_v ? c.vc : c.kc) + bh * c.block * c.D);
+  const float old = it.slot > 0 ? *scale : 0.0f;
+  float a = fmaxf(largest<FMT, BF16>(r0), largest<FMT, BF16>(r1));
+  for (int u = lane + 32; u < units; u += 32)
+    a = fmaxf(a, fmaxf(largest<FMT, BF16>(unit_at(u)[0]), largest<FMT, BF16>(unit_at(u)[1])));
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) a = fmaxf(a, __shfl_xor_sync(kAll, a, o));
+  constexpr float inv_q = FMT == kInt8 ? 1.0f / 127.0f : 1.0f / 448.0f;
+  const float S = fmaxf(old, fminf(fmaxf(a * inv_q, kScaleMin), kScaleMax));
+  const float inv = __fdiv_rn(1.0f, S);
+  __syncwarp();
+  if (lane == 0) *scale = S;
+  if (lane < units) codes[(it.slot << lu) + lane] = encode16<FMT, BF16>(r0, r1, inv);
+  for (int u = lane + 32; u < units; u += 32)
+    codes[(it.slot << lu) + u] = encode16<FMT, BF16>(unit_at(u)[0], unit_at(u)[1], inv);
+  if (it.slot > 0 && S > old) {
+    const float f = __fdiv_rn(old, S);
+#pragma unroll 4
+    for (int u = lane; u < (it.slot << lu); u += 32) codes[u] = recode16<FMT>(codes[u], f);
   }
 }
 
@@ -182,12 +263,13 @@ __global__ void __launch_bounds__(T) paged_write_kernel(Cache c, Tokens t, const
 template <int FMT, bool BF16, int T>
 __global__ void __launch_bounds__(T) paged_read_kernel(Cache c, Tokens t, uint16_t* __restrict__ k,
                                                        uint16_t* __restrict__ v) {
-  unsigned bad = 0;
-  const Item it = find_item(c, t, bad);
-  if (it.id < 0) return;
+  const Item it = find_block_item(c, t);
+  if (it.blk < 0) return;
+  const int id = find_block(c, it, threadIdx.x & 31);
+  if (id < 0) return;
   const int64_t stride = static_cast<int64_t>(c.Hkv) * c.D;
   uint16_t* x = (it.is_v ? v : k) + it.row * stride + static_cast<int64_t>(it.head) * c.D;
-  const int64_t bh = static_cast<int64_t>(it.id) * c.Hkv + it.head;
+  const int64_t bh = static_cast<int64_t>(id) * c.Hkv + it.head;
   const float S = (it.is_v ? c.vs : c.ks)[bh];
   const int upr = c.D >> 4, lu = 31 - __clz(upr);
   const uint4* codes = reinterpret_cast<const uint4*>((it.is_v ? c.vc : c.kc) + bh * c.block * c.D) + (it.slot << lu);
@@ -316,6 +398,10 @@ template <int FMT, bool BF16>
 void launch_write(const Cache& c, const Tokens& t, unsigned grid, const void* k, const void* v, int64_t ks, int64_t vs,
                   cudaStream_t st) {
   const uint16_t *kk = static_cast<const uint16_t*>(k), *vv = static_cast<const uint16_t*>(v);
+  if (t.n_tokens <= 2 * static_cast<int64_t>(c.B)) {
+    paged_append_kernel<FMT, BF16><<<(grid + 3) / 4, 128, 0, st>>>(c, t, grid, kk, vv, ks, vs);
+    return;
+  }
   switch (c.block * c.D >> 4) {                   // units of a full cache block
     case 64: case 128: paged_write_kernel<FMT, BF16, 128, 1><<<grid, 128, 0, st>>>(c, t, kk, vv, ks, vs); break;
     case 256: paged_write_kernel<FMT, BF16, 128, 2><<<grid, 128, 0, st>>>(c, t, kk, vv, ks, vs); break;

@@ -41,27 +41,71 @@ __device__ __forceinline__ int block_at(const Cache& c, int b, int64_t j, unsign
 }
 
 // Work items numbered without a prefix sum: sequence b of n_b rows has the
-// items floor(cu[b] / per) + slack * b onwards.  It may use floor(n_b / per) +
-// slack of them, since floor(x + n) - floor(x) >= floor(n); the last of them
-// may find nothing to do.  A warp searches 32 places at a time; with offsets
-// that do not ascend it ends at some sequence, whose ranges callers check.
-__device__ __forceinline__ int64_t item_base(const int32_t* cu, int b, int mul, int per, int slack) {
-  const int64_t x = cu[b];
-  return (x > 0 ? x * mul / per : 0) + static_cast<int64_t>(slack) * b;
+// items floor(cu[b] mul / per) + slack b onwards, per = 2^log_per.  It may use
+// floor(n_b mul / per) + slack of them, since floor(x + n) - floor(x) >=
+// floor(n); the last of them may find nothing to do.
+__device__ __forceinline__ int64_t item_base(int cu, int b, int mul, int log_per, int slack) {
+  return (cu > 0 ? (static_cast<int64_t>(cu) * mul) >> log_per : 0) + static_cast<int64_t>(slack) * b;
 }
-__device__ __forceinline__ int find_sequence(const int32_t* cu, int B, int64_t item, int mul, int per, int slack,
-                                             int lane) {
+
+// The sequence of an item: its number, offsets, entry of `more` (if given) and
+// the item's number in it.  A warp narrows the range 32 places at a time to
+// 128, and then looks at all of them at once: one load's latency for up to 128
+// sequences.  With offsets that do not ascend it ends at some sequence, whose
+// ranges callers check.
+struct Found {
+  int b, c0, c1, more;
+  int64_t item;
+};
+__device__ __forceinline__ Found find_sequence(const int32_t* cu, const int32_t* more, int B, int64_t item, int mul,
+                                               int log_per, int slack, int lane) {
   int lo = 0, hi = B;
-  while (hi - lo > 1) {
+  while (hi - lo > 128) {
     const int step = (hi - lo + 31) >> 5;
     const int at = lo + lane * step;
-    const bool le = at < hi && item_base(cu, at, mul, per, slack) <= item;
+    const bool le = at < hi && item_base(cu[at], at, mul, log_per, slack) <= item;
     int n = __popc(__ballot_sync(kAll, le));
     n = n < 1 ? 1 : n;
     lo += (n - 1) * step;
     hi = min(hi, lo + step);
   }
-  return lo;
+  Found f;
+  if (hi - lo < 32) {                             // few sequences: one load a lane
+    const int at = lo + lane;
+    const int x = at <= hi ? cu[at] : 0, y = more != nullptr && at < hi ? more[at] : 0;
+    int n = __popc(__ballot_sync(kAll, at < hi && item_base(x, at, mul, log_per, slack) <= item));
+    n = n < 1 ? 0 : n - 1;                        // the last place that qualifies
+    f.b = lo + n;
+    f.c0 = __shfl_sync(kAll, x, n);
+    f.c1 = __shfl_sync(kAll, x, n + 1);
+    f.more = __shfl_sync(kAll, y, n);
+  } else {
+    int x[4], y[4], n = 0;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int at = lo + 32 * k + lane;
+      x[k] = at <= hi ? cu[at] : 0;
+      y[k] = more != nullptr && at < hi ? more[at] : 0;
+    }
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int at = lo + 32 * k + lane;
+      n += __popc(__ballot_sync(kAll, at < hi && item_base(x[k], at, mul, log_per, slack) <= item));
+    }
+    n = n < 1 ? 0 : n - 1;
+    f.b = lo + n;
+    f.c0 = f.c1 = f.more = 0;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int u = __shfl_sync(kAll, x[k], n & 31), v = __shfl_sync(kAll, y[k], n & 31);
+      const int w = __shfl_sync(kAll, x[k], (n + 1) & 31);
+      if (n >> 5 == k) { f.c0 = u; f.more = v; }
+      if ((n + 1) >> 5 == k) f.c1 = w;
+    }
+    if (n == 127) f.c1 = cu[f.b + 1];
+  }
+  f.item = item - item_base(f.c0, f.b, mul, log_per, slack);
+  return f;
 }
 
 // ---- codes ----------------------------------------------------------------------

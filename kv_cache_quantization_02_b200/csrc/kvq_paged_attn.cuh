@@ -75,14 +75,16 @@ __device__ __forceinline__ int row_exponent(float most) {
 __device__ __forceinline__ float pow2i(int k) { return __uint_as_float(static_cast<uint32_t>(k + 127) << 23); }
 
 // A sequence's length, clamped to its table row.
-__device__ __forceinline__ int sequence_length(const AttnArgs& a, int b, unsigned& bad) {
+__device__ __forceinline__ int clamped_length(const AttnArgs& a, int L, unsigned& bad) {
   const int room = a.c.max_blocks << a.c.log_block;
-  int L = a.seq_len[b];
   if (L < 0 || L > room) {
     bad |= kFaultLength;
     L = L < 0 ? 0 : room;
   }
   return L;
+}
+__device__ __forceinline__ int sequence_length(const AttnArgs& a, int b, unsigned& bad) {
+  return clamped_length(a, a.seq_len[b], bad);
 }
 
 }  // namespace kvqp

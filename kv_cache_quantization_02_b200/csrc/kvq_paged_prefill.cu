@@ -61,7 +61,7 @@ struct Prefill {
   static constexpr int MT = D == 256 ? 1 : 2;     // 128-row tiles
   static constexpr int KT = D == 256 ? 64 : 128;  // keys of a tile in shared memory
   static constexpr int STEPS = KT / kStep;        // steps of a tile
-  static constexpr int ROWS = MT * 128;
+  static constexpr int ROWS = MT * 128, LOG_ROWS = MT == 2 ? 8 : 7;
   static constexpr int CB = D / 64;               // 64-channel blocks (128-byte swizzled rows)
   static constexpr int NSUB = KT / 16;            // 16-key parts, each inside one cache block
   static constexpr int QBYTES = ROWS * D * 2;
@@ -185,9 +185,9 @@ __device__ __forceinline__ bool find_job(const AttnArgs& a, int nsplit, Job& j, 
   // the last tiles of a sequence see most keys: they start first
   const int64_t items = a.total_q * a.R / C::ROWS + a.c.B;
   const int64_t item = items - 1 - x / a.c.Hkv;
-  j.b = find_sequence(a.cu, a.c.B, item, a.R, C::ROWS, 1, threadIdx.x & 31);
-  const int64_t k = item - item_base(a.cu, j.b, a.R, C::ROWS, 1);
-  const int64_t c0 = a.cu[j.b], c1 = a.cu[j.b + 1];
+  const Found f = find_sequence(a.cu, a.seq_len, a.c.B, item, a.R, C::LOG_ROWS, 1, threadIdx.x & 31);
+  j.b = f.b;
+  const int64_t k = f.item, c0 = f.c0, c1 = f.c1;
   if (c0 < 0 || c1 < c0 || c1 > a.total_q) {
     bad |= kFaultLength;
     return false;
@@ -198,7 +198,7 @@ __device__ __forceinline__ bool find_job(const AttnArgs& a, int nsplit, Job& j, 
   if (k < 0 || k * C::ROWS >= rows) return false;
   j.row0 = static_cast<int>(k * C::ROWS);
   j.count = static_cast<int>(min(static_cast<int64_t>(C::ROWS), rows - j.row0));
-  j.L = sequence_length(a, j.b, bad);
+  j.L = clamped_length(a, f.more, bad);
   const int p0 = j.L - j.n + j.row0 / a.R, p1 = j.L - j.n + (j.row0 + j.count - 1) / a.R;
   j.lo = a.window > 0 ? max(0, p0 - a.window + 1) : 0;
   j.hi = max(0, p1 + 1);
@@ -647,9 +647,8 @@ __global__ void __launch_bounds__(256) paged_prefill_join_kernel(AttnArgs a, int
   const int r = static_cast<int>(blockIdx.x % PERTILE) * 8 + (threadIdx.x >> 5);
   const int64_t items = a.total_q * a.R / C::ROWS + a.c.B, item = items - 1 - tile / a.c.Hkv;
   const int kvh = static_cast<int>(tile % a.c.Hkv);
-  const int b = find_sequence(a.cu, a.c.B, item, a.R, C::ROWS, 1, lane);
-  const int64_t k = item - item_base(a.cu, b, a.R, C::ROWS, 1), c0 = a.cu[b], c1 = a.cu[b + 1];
-  const int64_t row = k * C::ROWS + r;
+  const Found at = find_sequence(a.cu, nullptr, a.c.B, item, a.R, C::LOG_ROWS, 1, lane);
+  const int64_t k = at.item, c0 = at.c0, c1 = at.c1, row = k * C::ROWS + r;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   if (c0 < 0 || c1 < c0 || c1 > a.total_q || k < 0 || row >= (c1 - c0) * a.R) return;
   float o[DPL], m = -INFINITY, l = 0.0f;

@@ -17,6 +17,7 @@ library is missing, importing this module raises ImportError.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 import torch  # loads libcudart first, so the library shares torch's runtime
@@ -488,6 +489,11 @@ def dequantize(packed: torch.Tensor, scales: torch.Tensor, lam: torch.Tensor,
 _PAGED_FORMAT = {torch.int8: KVQ_INT8, torch.float8_e4m3fn: KVQ_E4M3}
 _PAGED_DTYPE = {torch.float16: KVQ_FP16, torch.bfloat16: KVQ_BF16}
 
+# torch.cuda.current_device() and the handle of current_stream(index) without
+# the objects around them (a microsecond a call)
+_current_device = torch._C._cuda_getDevice
+_current_stream = torch._C._cuda_getCurrentRawStream
+
 
 def _paged_need(t, dtype, shape, index, name):
     """`t` is a contiguous tensor of this type and shape on CUDA device `index`."""
@@ -534,12 +540,12 @@ def _paged_rows(x, name, D, index):
 
 
 def _paged_call(index, fn, *args):
-    """fn(*args, stream) on the device's current stream; raises KvqError."""
-    if index == torch.cuda.current_device():
-        rc = fn(*args, torch.cuda.current_stream(index).cuda_stream)
+    """fn(*args) with device `index` current; raises KvqError."""
+    if index == _current_device():
+        rc = fn(*args)
     else:
         with torch.cuda.device(index):
-            rc = fn(*args, torch.cuda.current_stream(index).cuda_stream)
+            rc = fn(*args)
     if rc != KVQ_OK:
         raise KvqError(rc)
 
@@ -579,7 +585,8 @@ def paged_write(k: torch.Tensor, v: torch.Tensor, cu_tokens: torch.Tensor, start
     _paged_need(start, torch.int32, (B,), index, "start")
     _paged_call(index, _lib.kvq_paged_write, k.data_ptr(), v.data_ptr(), dtype, k_stride, v_stride,
                 cu_tokens.data_ptr(), start.data_ptr(), block_table.data_ptr(), B, max_blocks, n, Hkv, D, block, fmt,
-                num_blocks, k_cache.data_ptr(), v_cache.data_ptr(), k_scales.data_ptr(), v_scales.data_ptr())
+                num_blocks, k_cache.data_ptr(), v_cache.data_ptr(), k_scales.data_ptr(), v_scales.data_ptr(),
+                _current_stream(index))
 
 
 def paged_read(cu_tokens: torch.Tensor, start: torch.Tensor, block_table: torch.Tensor, k_cache: torch.Tensor,
@@ -609,14 +616,21 @@ def paged_read(cu_tokens: torch.Tensor, start: torch.Tensor, block_table: torch.
         _paged_need(v_out, dtype, shape, index, "v_out")
     _paged_call(index, _lib.kvq_paged_read, cu_tokens.data_ptr(), start.data_ptr(), block_table.data_ptr(), B,
                 max_blocks, n_tokens, Hkv, D, block, fmt, num_blocks, k_cache.data_ptr(), v_cache.data_ptr(),
-                k_scales.data_ptr(), v_scales.data_ptr(), code, k_out.data_ptr(), v_out.data_ptr())
+                k_scales.data_ptr(), v_scales.data_ptr(), code, k_out.data_ptr(), v_out.data_ptr(),
+                _current_stream(index))
     return k_out, v_out
+
+
+@functools.lru_cache(maxsize=4096)
+def _paged_workspace_bytes(index, *shape):
+    with torch.cuda.device(index):
+        return _lib.kvq_paged_workspace_bytes(*shape)
 
 
 def _paged_workspace(workspace, like, index, *shape):
     """(tensor or None, address, bytes): `workspace` True allocates what the library asks for."""
     if workspace is True:
-        need = _lib.kvq_paged_workspace_bytes(*shape)
+        need = _paged_workspace_bytes(index, *shape)
         if need <= 0:
             return None, 0, 0
         workspace = like.new_empty(need, dtype=torch.uint8)
@@ -653,7 +667,7 @@ def paged_attention_decode(q: torch.Tensor, seq_len: torch.Tensor, block_table: 
     _paged_call(index, _lib.kvq_paged_attention_decode, q.data_ptr(), dtype, q_stride, seq_len.data_ptr(),
                 block_table.data_ptr(), B, max_blocks, Hq, Hkv, D, block, fmt, num_blocks, k_cache.data_ptr(),
                 v_cache.data_ptr(), k_scales.data_ptr(), v_scales.data_ptr(), sm_scale, window, out.data_ptr(), ws_ptr,
-                ws_bytes)
+                ws_bytes, _current_stream(index))
     return out
 
 
@@ -682,5 +696,5 @@ def paged_attention_prefill(q: torch.Tensor, cu_q: torch.Tensor, seq_len: torch.
     _paged_call(index, _lib.kvq_paged_attention_prefill, q.data_ptr(), dtype, q_stride, cu_q.data_ptr(),
                 seq_len.data_ptr(), block_table.data_ptr(), B, max_blocks, n, Hq, Hkv, D, block, fmt, num_blocks,
                 k_cache.data_ptr(), v_cache.data_ptr(), k_scales.data_ptr(), v_scales.data_ptr(), sm_scale, window,
-                out.data_ptr(), ws_ptr, ws_bytes)
+                out.data_ptr(), ws_ptr, ws_bytes, _current_stream(index))
     return out
