@@ -36,10 +36,11 @@ struct AttnArgs {
   float scale;              // |sm_scale| log2(e)
 };
 
-// A code pair as fp16: the bytes at bits 0-7 and 16-23 (even) or 8-15 and
-// 24-31 (odd) of a word.  int8: the code plus 128 in the low byte of 1024's
-// significand, exact, less 1152.  e4m3: exponent and significand moved to
-// fp16's places, which gives the value times 2^-8, exact, subnormals too.
+// A code pair as fp16, exact: the bytes at bits 0-7 and 16-23 (even) or 8-15
+// and 24-31 (odd) of a word.  int8: the code plus 128 in the low byte of 1024's
+// significand, less 1152.  e4m3: a conversion of two neighbouring bytes; it
+// makes NaN of the NaN pattern, so slots behind a sequence's last position,
+// which may hold anything, have to arrive as zeros (0 x NaN is NaN).
 template <int FMT>
 __device__ __forceinline__ void codes_to_half2(uint32_t w, uint32_t& even, uint32_t& odd) {
   if constexpr (FMT == kInt8) {
@@ -48,14 +49,11 @@ __device__ __forceinline__ void codes_to_half2(uint32_t w, uint32_t& even, uint3
     asm("sub.f16x2 %0, %1, %2;" : "=r"(even) : "r"(e), "r"(0x64806480u));
     asm("sub.f16x2 %0, %1, %2;" : "=r"(odd) : "r"(o), "r"(0x64806480u));
   } else {
-    const uint32_t v = w << 8;
-    even = ((v >> 1) & 0x3F803F80u) | (v & 0x80008000u);
-    odd = ((w >> 1) & 0x3F803F80u) | (w & 0x80008000u);
+    const uint32_t p = __byte_perm(w, 0u, 0x3120);
+    asm("{\n.reg .b16 l, h;\nmov.b32 {l, h}, %2;\ncvt.rn.f16x2.e4m3x2 %0, l;\ncvt.rn.f16x2.e4m3x2 %1, h;\n}"
+        : "=r"(even), "=r"(odd) : "r"(p));
   }
 }
-// What codes_to_half2 leaves to multiply by.
-template <int FMT>
-constexpr float kCodeUnit = FMT == kInt8 ? 1.0f : 256.0f;
 
 // 2^x by the SFU (relative error about 2^-22, results below 2^-126 are 0).
 __device__ __forceinline__ float exp2_approx(float x) {

@@ -63,6 +63,10 @@ __device__ __forceinline__ uint32_t smem_u32(const void* p) {
 __device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" :: "r"(dst), "l"(src) : "memory");
 }
+// With `bytes` 0 the 16 bytes become zeros and src is not read.
+__device__ __forceinline__ void copy16_or_zeros(uint32_t dst, const void* src, int bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" :: "r"(dst), "l"(src), "r"(bytes) : "memory");
+}
 __device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
 __device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_group %0;" :: "n"(N) : "memory"); }
@@ -261,6 +265,7 @@ __global__ void __launch_bounds__(kWarps * 32, Decode<D>::BLOCKS) paged_decode_k
   // differs from copy 0's by a constant of i.
   const uint32_t put = place<D>(lane * 16 / D, lane & (NCH - 1));
   auto mix = [](int i) -> uint32_t { return D == 64 ? 0u : D == 128 ? (i & 1) * 64u : (i & 3) * 32u; };
+  int live = 0;                                   // keys from the tile's first to the sequence's end
   auto load_half = [&]() {                        // one half-tile into the ring's next place
     if (!vnext) {
       while (more && lt >= lp.tb) {
@@ -299,6 +304,7 @@ __global__ void __launch_bounds__(kWarps * 32, Decode<D>::BLOCKS) paged_decode_k
           }
         }
         const int cur0 = __shfl_sync(kAll, id0, at), cur1 = __shfl_sync(kAll, id1, at);
+        live = lp.s.L - (lp.s.first + lt * kTile);
         const int slot0 = (lp.s.first + lt * kTile) & (block - 1), slot1 = (slot0 + 16) & (block - 1);
         src0 = cur0 < 0 ? -1 : static_cast<int64_t>((cur0 * a.c.Hkv + kvh) * block + slot0) * D + lane * 16;
         src1 = cur1 < 0 ? -1 : static_cast<int64_t>((cur1 * a.c.Hkv + kvh) * block + slot1) * D + lane * 16;
@@ -308,13 +314,22 @@ __global__ void __launch_bounds__(kWarps * 32, Decode<D>::BLOCKS) paged_decode_k
     }
     const uint8_t* codes = vnext ? a.c.vc : a.c.kc;
     const uint32_t dst = ring + lslot * C::HALF;
-    if (src0 >= 0) {
+    if (FMT == kInt8 || (more && live >= kTile && src0 >= 0 && src1 >= 0)) {
+      if (src0 >= 0) {
 #pragma unroll
-      for (int i = 0; i < NCH / 2; ++i) copy16(dst + (put ^ mix(i)) + i * 512, codes + src0 + i * 512);
-    }
-    if (src1 >= 0) {
+        for (int i = 0; i < NCH / 2; ++i) copy16(dst + (put ^ mix(i)) + i * 512, codes + src0 + i * 512);
+      }
+      if (src1 >= 0) {
 #pragma unroll
-      for (int i = NCH / 2; i < NCH; ++i) copy16(dst + (put ^ mix(i)) + i * 512, codes + src1 + (i - NCH / 2) * 512);
+        for (int i = NCH / 2; i < NCH; ++i) copy16(dst + (put ^ mix(i)) + i * 512, codes + src1 + (i - NCH / 2) * 512);
+      }
+    } else if (more) {                            // e4m3: zeros where there is nothing to see
+#pragma unroll
+      for (int i = 0; i < NCH; ++i) {
+        const int64_t src = i < NCH / 2 ? src0 + i * 512 : src1 + (i - NCH / 2) * 512;
+        const bool there = (i < NCH / 2 ? src0 : src1) >= 0 && (i * 512 + lane * 16) / D < live;
+        copy16_or_zeros(dst + (put ^ mix(i)) + i * 512, codes + (there ? src : 0), there ? 16 : 0);
+      }
     }
     copies_commit();
     if (!vnext && more) {
@@ -348,7 +363,7 @@ __global__ void __launch_bounds__(kWarps * 32, Decode<D>::BLOCKS) paged_decode_k
       uint2 raw[NCH];
 #pragma unroll
       for (int c = 0; c < NCH; ++c) raw[c] = g < heads ? *reinterpret_cast<const uint2*>(q + 16 * c) : make_uint2(0, 0);
-      float unit = a.scale * kCodeUnit<FMT>;
+      float unit = a.scale;
       if (a.bf16) {
         float most = 0.0f;
 #pragma unroll
@@ -544,7 +559,7 @@ __global__ void __launch_bounds__(kWarps * 32, Decode<D>::BLOCKS) paged_decode_k
         if (h >= heads) continue;
         if (whole) {
           // no key: 0; NaN stays
-          const float inv = l_all[j] == 0.0f ? 0.0f : kCodeUnit<FMT> / l_all[j];
+          const float inv = l_all[j] == 0.0f ? 0.0f : 1.0f / l_all[j];
           uint16_t* o = a.out + (static_cast<int64_t>(p.b) * a.c.Hkv * a.R + kvh * a.R + h0 + h) * D + 2 * g;
 #pragma unroll
           for (int i = 0; i < NCH; ++i)
@@ -647,7 +662,7 @@ __global__ void __launch_bounds__(kWarps * 32) paged_decode_join_kernel(AttnArgs
     f[w] = exp2_approx(sums[w][D] - ref);
     l = fmaf(sums[w][D + 1], f[w], l);
   }
-  const float inv = l == 0.0f ? 0.0f : kCodeUnit<FMT> / l;
+  const float inv = l == 0.0f ? 0.0f : 1.0f / l;
   uint16_t* out = a.out + (static_cast<int64_t>(head.x) * a.c.Hkv * a.R + kvh * a.R + h0 + h) * D;
   for (int i = 2 * threadIdx.x; i < D; i += 2 * kWarps * 32) {
     float u = 0.0f, v = 0.0f;

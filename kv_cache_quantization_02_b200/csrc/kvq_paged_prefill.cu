@@ -232,7 +232,9 @@ struct Share {
   static constexpr int N = C::KT * D / 1024;
   static constexpr int PERPART = D / 16;          // chunks of a 16-key part
   uint2 w[N];
-  __device__ __forceinline__ void load(const uint8_t* codes, int rows, int which, int lane) {
+  // (e4m3: keys from `live` on, behind the sequence's last, as zeros)
+  template <int FMT>
+  __device__ __forceinline__ void load(const uint8_t* codes, int rows, int live, int which, int lane) {
     const uint8_t* mine = codes + which * 256 + lane * 8;
     const uint8_t* p = nullptr;
 #pragma unroll
@@ -241,7 +243,8 @@ struct Share {
         const int row = __shfl_sync(kAll, rows, 4 * i / PERPART);
         p = row < 0 ? nullptr : mine + static_cast<int64_t>(row) * D;
       }
-      w[i] = p ? __ldg(reinterpret_cast<const uint2*>(p + 4 * i % PERPART * 256)) : make_uint2(0, 0);
+      const bool there = p != nullptr && (FMT == kInt8 || ((4 * i + which) * 32 + lane) / (D / 8) < live);
+      w[i] = there ? __ldg(reinterpret_cast<const uint2*>(p + 4 * i % PERPART * 256)) : make_uint2(0, 0);
     }
   }
   // To the tile at dst: row r, 8-channel unit c at unit (c mod 8) ^ (r mod 8) of
@@ -321,7 +324,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_prefill_kernel(AttnArgs a, 
 #pragma unroll
     for (int n = 0; n < N; ++n) {
       const int r = n * W + warp * AT_ONCE + lane / LANES;
-      float u = a.scale * kCodeUnit<FMT>;
+      float u = a.scale;
       uint32_t h[4] = {w[n].x, w[n].y, w[n].z, w[n].w};
       if (a.bf16) {
         float2 x[4];
@@ -461,7 +464,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_prefill_kernel(AttnArgs a, 
       // ---- outputs
       if (j.steps > 0 && wait(&o_full[mt * 2 + ((j.steps - 1) & 1)], ((j.steps - 1) >> 1) & 1)) tmem_fence_after();
       const bool some = j.steps > 0 && ok;
-      const float inv = l == 0.0f ? 0.0f : kCodeUnit<FMT> / l;
+      const float inv = l == 0.0f ? 0.0f : 1.0f / l;
       if (ok && nsplit > 1) {
         float* part = a.part + ((j.tile * nsplit + j.split) * C::ROWS + r) * (D + 4);
 #pragma unroll 1
@@ -598,7 +601,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_prefill_kernel(AttnArgs a, 
       int rows = -1, rows2 = -1;                  // the parts of the tile in `next`, and of the one after it
       if (j.tiles > 0) {
         rows = part_row<D>(a, j, j.first, lane, bad);
-        next.load(codes, rows, which, lane);
+        next.template load<FMT>(codes, rows, j.L - j.first, which, lane);
         if (j.tiles > 1) rows2 = part_row<D>(a, j, j.first + KT, lane, bad);
       }
 #pragma unroll 1
@@ -621,7 +624,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_prefill_kernel(AttnArgs a, 
         __syncwarp();
         if (lane == 0) mbar_arrive(&full[st]);
         rows = rows2;
-        if (i + 1 < j.tiles) next.load(codes, rows, which, lane);
+        if (i + 1 < j.tiles) next.template load<FMT>(codes, rows, j.L - j.first - (i + 1) * KT, which, lane);
         if (i + 2 < j.tiles) rows2 = part_row<D>(a, j, j.first + (i + 2) * KT, lane, bad);
       }
     }
@@ -669,7 +672,7 @@ __global__ void __launch_bounds__(256) paged_prefill_join_kernel(AttnArgs a, int
     }
     m = now;
   }
-  const float inv = l == 0.0f ? 0.0f : kCodeUnit<FMT> / l;
+  const float inv = l == 0.0f ? 0.0f : 1.0f / l;
   uint16_t* out = a.out + ((c0 + row / a.R) * a.c.Hkv * a.R + kvh * a.R + row % a.R) * D + lane * DPL;
 #pragma unroll
   for (int i = 0; i < DPL; i += 2)
