@@ -329,13 +329,15 @@ int sm_count() {
 }
 
 // Thread blocks of a split decode call: all that the GPU holds at once, or one
-// per four tiles of 32 keys if the table has room for fewer.
-int decode_grid(int B, int max_blocks, int Hq, int Hkv, int D, int block) {
+// per four tiles of 32 keys if the table has room, or the window, for fewer.
+int decode_grid(int B, int max_blocks, int Hq, int Hkv, int D, int block, int window) {
   const int64_t items = static_cast<int64_t>(B) * Hkv * ((Hq / Hkv + 7) / 8);
-  const int64_t tiles = (static_cast<int64_t>(max_blocks) * block + 31) / 32 + 1;
-  const int64_t full = static_cast<int64_t>(sm_count()) * (D <= 128 ? 3 : 2);
+  int64_t tiles = (static_cast<int64_t>(max_blocks) * block + 31) / 32 + 1;
+  if (window > 0 && window / 32 + 2 < tiles) tiles = window / 32 + 2;
+  const int64_t full = static_cast<int64_t>(sm_count()) *
+                       (D == 64 ? kDecodeBlocks<64> : D == 128 ? kDecodeBlocks<128> : kDecodeBlocks<256>);
   if (items >= full) return static_cast<int>(full);
-  const int64_t most = (items * tiles + 3) / 4;
+  const int64_t most = items * ((tiles + 3) / 4);
   return static_cast<int>(most < full ? most : full);
 }
 int64_t decode_bytes(int grid, int D) { return static_cast<int64_t>(grid) * (2 * 8 * (D + 4) * 4 + 16); }
@@ -529,7 +531,7 @@ int kvq_paged_read(const int32_t* cu_tokens, const int32_t* start, const int32_t
 int64_t kvq_paged_workspace_bytes(int B, int max_blocks, int64_t total_q, int Hq, int Hkv, int D, int block) {
   if (check_shape(KVQ_FP16, KVQ_INT8, B, max_blocks, Hkv, D, block, 0) != KVQ_OK) return -1;
   if (Hq < Hkv || Hq % Hkv != 0 || total_q < 0 || total_q > INT32_MAX || total_q * Hq > INT32_MAX) return -1;
-  const int64_t one = decode_bytes(decode_grid(B, max_blocks, Hq, Hkv, D, block), D);
+  const int64_t one = decode_bytes(decode_grid(B, max_blocks, Hq, Hkv, D, block, 0), D);
   const int64_t many = prompt_grid(B, max_blocks, total_q, Hq, Hkv, D, block, 0).bytes;
   return one > many ? one : many;
 }
@@ -543,7 +545,7 @@ int kvq_paged_attention_decode(const void* q, int dtype, int64_t q_stride, const
   const int rc = attention_args(p, q, dtype, q_stride, nullptr, seq_len, block_table, B, max_blocks, B, Hq, Hkv, D,
                                 block, format, num_blocks, k_codes, v_codes, k_scales, v_scales, sm_scale, window, out);
   if (rc != KVQ_OK || p.q == nullptr) return rc;
-  const int grid = decode_grid(B, max_blocks, Hq, Hkv, D, block);
+  const int grid = decode_grid(B, max_blocks, Hq, Hkv, D, block, window);
   if (grid > 0 && workspace && aligned_to(workspace, 16) && workspace_bytes >= decode_bytes(grid, D))
     p.part = static_cast<float*>(workspace);
   p.blocks = grid;

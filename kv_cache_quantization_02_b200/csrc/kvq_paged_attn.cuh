@@ -22,6 +22,11 @@ namespace kvqp {
 
 constexpr float kBoost = 6.0f, kLazy = 8.0f;
 
+// Thread blocks of the decode kernel that an SM holds (registers and shared
+// memory); a split call launches that many for each SM.
+template <int D>
+constexpr int kDecodeBlocks = D == 64 ? 4 : 3;
+
 struct AttnArgs {
   Cache c;
   const uint16_t* q;

@@ -47,13 +47,13 @@ constexpr int kMetaSlots = 8;                     // tiles whose scales are kept
 template <int D>
 struct Decode {
   static constexpr int HALF = kTile * D;          // bytes of one half-tile: 32 keys of K, or of V
-  static constexpr int NST = D == 64 ? 8 : D == 128 ? 4 : 3;
+  static constexpr int NST = D == 64 ? 4 : 2;
   static constexpr int RING = kWarps * NST * HALF;
-  static constexpr int XCH = 2 * kHeads * D * 4;  // two warps' sums while a block joins its warps
+  static constexpr int XP = D == 256 ? 2 : 1;     // parts in which a block joins its warps' sums
+  static constexpr int XCH = 2 * kHeads * D * 4 / XP;       // two warps' sums of a part
   static constexpr int META = kWarps * kMetaSlots * 32;
   static constexpr int ML = kWarps * kHeads * 8;
   static constexpr int SMEM = RING + XCH + META + ML + 128;
-  static constexpr int BLOCKS = D <= 128 ? 3 : 2; // per SM: 216 KB (D 256: 225 KB) of shared memory
   static constexpr int NCH = D / 16;              // 16-channel steps
 };
 
@@ -113,30 +113,41 @@ __device__ __forceinline__ Span span_of(const AttnArgs& a, int b, unsigned& bad)
 }
 
 // One scan over the lengths, a run of sequences a thread: the tiles before this
-// thread's run (b0 .. b1), and all tiles.
-__device__ __forceinline__ int64_t scan_tiles(const AttnArgs& a, int tid, int nt, int& b0, int& b1, int64_t& total,
-                                              int64_t* sums, unsigned& bad) {
-  const int run = (a.c.B + nt - 1) / nt;
+// thread's run (b0 .. b1), and all tiles; likewise with every sequence's tiles
+// rounded up to a whole number of warps' rounds.
+struct Sums {
+  int64_t tiles, rounded;
+};
+__device__ __forceinline__ int rounded(int tiles) { return (tiles + kWarps - 1) & ~(kWarps - 1); }
+__device__ __forceinline__ Sums scan_tiles(const AttnArgs& a, int tid, int& b0, int& b1, Sums& total, int64_t* sums,
+                                           unsigned& bad) {
+  const int run = (a.c.B + kWarps * 32 - 1) / (kWarps * 32);
   b0 = min(a.c.B, tid * run);
   b1 = min(a.c.B, b0 + run);
-  int64_t mine = 0;
-  for (int b = b0; b < b1; ++b) mine += span_of(a, b, bad).tiles;
+  int64_t mine = 0, mine_r = 0;
+  for (int b = b0; b < b1; ++b) {
+    const int n = span_of(a, b, bad).tiles;
+    mine += n;
+    mine_r += rounded(n);
+  }
   const int lane = tid & 31, w = tid >> 5;
-  int64_t inc = mine;
+  int64_t inc = mine, inc_r = mine_r;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const int64_t x = __shfl_up_sync(kAll, inc, o);
-    if (lane >= o) inc += x;
+    const int64_t x = __shfl_up_sync(kAll, inc, o), y = __shfl_up_sync(kAll, inc_r, o);
+    if (lane >= o) { inc += x; inc_r += y; }
   }
-  if (lane == 31) sums[w] = inc;
+  if (lane == 31) { sums[w] = inc; sums[kWarps + w] = inc_r; }
   __syncthreads();
-  int64_t before = 0;
-  total = 0;
-  for (int i = 0; i < nt / 32; ++i) {
-    if (i < w) before += sums[i];
-    total += sums[i];
+  Sums before = {inc - mine, inc_r - mine_r};
+  total = {0, 0};
+#pragma unroll
+  for (int i = 0; i < kWarps; ++i) {
+    if (i < w) { before.tiles += sums[i]; before.rounded += sums[kWarps + i]; }
+    total.tiles += sums[i];
+    total.rounded += sums[kWarps + i];
   }
-  return before + inc - mine;
+  return before;
 }
 // Tiles of one stretch: an equal share, but at least one for every warp.
 __device__ __forceinline__ int64_t share_of(int64_t tiles, int blocks) {
@@ -194,14 +205,14 @@ __device__ __forceinline__ void write_empty(const AttnArgs& a, unsigned& bad) {
 }
 
 template <int D, int FMT>
-__global__ void __launch_bounds__(kWarps * 32, Decode<D>::BLOCKS) paged_decode_kernel(AttnArgs a) {
+__global__ void __launch_bounds__(kWarps * 32, kDecodeBlocks<D>) paged_decode_kernel(AttnArgs a) {
   using C = Decode<D>;
   constexpr int NST = C::NST, NCH = C::NCH;
   extern __shared__ __align__(1024) uint8_t sm[];
-  float4* xch = reinterpret_cast<float4*>(sm + C::RING);                       // [2][NCH][32]
+  float4* xch = reinterpret_cast<float4*>(sm + C::RING);                       // [2][NCH / XP][32]
   float4* meta = reinterpret_cast<float4*>(sm + C::RING + C::XCH);             // [warp][slot]
   float2* ml = reinterpret_cast<float2*>(sm + C::RING + C::XCH + C::META);     // [warp][head]
-  int64_t* sums = reinterpret_cast<int64_t*>(sm + C::RING + C::XCH + C::META + C::ML);   // [4], then the start
+  int64_t* sums = reinterpret_cast<int64_t*>(sm + C::RING + C::XCH + C::META + C::ML);   // [8], then the start
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int g = lane >> 2, t = lane & 3;
   const int groups = (a.R + kHeads - 1) / kHeads, items = a.c.Hkv * groups;
@@ -215,31 +226,37 @@ __global__ void __launch_bounds__(kWarps * 32, Decode<D>::BLOCKS) paged_decode_k
   int64_t share = 0;
   if (a.part != nullptr) {
     int b0, b1;
-    int64_t total;
-    const int64_t before = scan_tiles(a, tid, kWarps * 32, b0, b1, total, sums, bad);
-    const int64_t all = total * items, w0 = blockIdx.x * (share = share_of(all, gridDim.x));
+    Sums total;
+    const Sums before = scan_tiles(a, tid, b0, b1, total, sums, bad);
+    // With little to do a stretch is one round of the warps inside one item (the
+    // line then counts every item as whole rounds); else an equal share.
+    const bool few = total.rounded * items <= static_cast<int64_t>(gridDim.x) * kWarps;
+    const int64_t all = (few ? total.rounded : total.tiles) * items;
+    share = few ? kWarps : share_of(all, gridDim.x);
+    const int64_t w0 = blockIdx.x * share;
     if (tid == 0) *head_at<D>(a, blockIdx.x) = make_int4(0, 0, 0, 0);
     write_empty(a, bad);
     if (w0 >= all) {
       if (bad) atomicOr(&g_decode_fault, bad);
       return;
     }
-    int64_t at = before;
+    int64_t at = few ? before.rounded : before.tiles;
     for (int b = b0; b < b1; ++b) {
-      const Span s = span_of(a, b, bad);
-      if (at * items <= w0 && w0 < (at + s.tiles) * items) {       // one thread finds it
-        sums[4] = b;
-        sums[5] = w0 - at * items;
+      const int tiles = span_of(a, b, bad).tiles, n = few ? rounded(tiles) : tiles;
+      if (at * items <= w0 && w0 < (at + n) * items) {             // one thread finds it
+        sums[2 * kWarps] = b;
+        sums[2 * kWarps + 1] = w0 - at * items;
       }
-      at += s.tiles;
+      at += n;
     }
     __syncthreads();
-    p.b = static_cast<int>(sums[4]);
-    const int64_t off = sums[5];
+    p.b = static_cast<int>(sums[2 * kWarps]);
+    const int64_t off = sums[2 * kWarps + 1];
     p.s = span_of(a, p.b, bad);
-    p.item = static_cast<int>(off / p.s.tiles);
-    p.ta = static_cast<int>(off % p.s.tiles);
-    p.left = min(share, all - w0);
+    const int n = few ? rounded(p.s.tiles) : p.s.tiles;
+    p.item = static_cast<int>(off / n);
+    p.ta = static_cast<int>(off % n);
+    p.left = few ? min(kWarps, p.s.tiles - p.ta) : min(share, all - w0);
   } else {
     p.b = blockIdx.x / items;
     p.item = blockIdx.x % items;
@@ -525,27 +542,38 @@ __global__ void __launch_bounds__(kWarps * 32, Decode<D>::BLOCKS) paged_decode_k
         O[i][2 + j] *= f;
       }
     }
-    if (warp >= 2) {
 #pragma unroll
-      for (int i = 0; i < NCH; ++i)
-        xch[((warp - 2) * NCH + i) * 32 + lane] = make_float4(O[i][0], O[i][1], O[i][2], O[i][3]);
-    }
-    __syncthreads();
-    if (warp < 2) {
+    for (int part = 0; part < C::XP; ++part) {
+      constexpr int N = NCH / C::XP;
+      if (warp >= 2) {
 #pragma unroll
-      for (int i = 0; i < NCH; ++i) {
-        const float4 x = xch[(warp * NCH + i) * 32 + lane];
-        O[i][0] += x.x; O[i][1] += x.y; O[i][2] += x.z; O[i][3] += x.w;
-        if (warp == 1) xch[(NCH + i) * 32 + lane] = make_float4(O[i][0], O[i][1], O[i][2], O[i][3]);
+        for (int i = 0; i < N; ++i) {
+          const float(&o)[4] = O[part * N + i];
+          xch[((warp - 2) * N + i) * 32 + lane] = make_float4(o[0], o[1], o[2], o[3]);
+        }
       }
+      __syncthreads();
+      if (warp < 2) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+          float(&o)[4] = O[part * N + i];
+          const float4 x = xch[(warp * N + i) * 32 + lane];
+          o[0] += x.x; o[1] += x.y; o[2] += x.z; o[3] += x.w;
+          if (warp == 1) xch[(N + i) * 32 + lane] = make_float4(o[0], o[1], o[2], o[3]);
+        }
+      }
+      __syncthreads();
+      if (warp == 0) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+          float(&o)[4] = O[part * N + i];
+          const float4 x = xch[(N + i) * 32 + lane];
+          o[0] += x.x; o[1] += x.y; o[2] += x.z; o[3] += x.w;
+        }
+      }
+      if (part + 1 < C::XP) __syncthreads();
     }
-    __syncthreads();
     if (warp == 0) {
-#pragma unroll
-      for (int i = 0; i < NCH; ++i) {
-        const float4 x = xch[(NCH + i) * 32 + lane];
-        O[i][0] += x.x; O[i][1] += x.y; O[i][2] += x.z; O[i][3] += x.w;
-      }
       const bool whole = p.ta == 0 && p.tb == p.s.tiles;
       // a stretch's first and last piece may be parts of an item; the one that
       // begins an item and does not end it says where its other parts are
