@@ -225,33 +225,56 @@ __global__ void __launch_bounds__(kWarps * 32, kDecodeBlocks<D>) paged_decode_ke
   Piece p;
   int64_t share = 0;
   if (a.part != nullptr) {
-    int b0, b1;
-    Sums total;
-    const Sums before = scan_tiles(a, tid, b0, b1, total, sums, bad);
     // With little to do a stretch is one round of the warps inside one item (the
     // line then counts every item as whole rounds); else an equal share.
-    const bool few = total.rounded * items <= static_cast<int64_t>(gridDim.x) * kWarps;
-    const int64_t all = (few ? total.rounded : total.tiles) * items;
-    share = few ? kWarps : share_of(all, gridDim.x);
-    const int64_t w0 = blockIdx.x * share;
-    if (tid == 0) *head_at<D>(a, blockIdx.x) = make_int4(0, 0, 0, 0);
-    write_empty(a, bad);
+    bool few;
+    int64_t all, w0, off;
+    auto lay_out = [&](const Sums& total) {
+      few = total.rounded * items <= static_cast<int64_t>(gridDim.x) * kWarps;
+      all = (few ? total.rounded : total.tiles) * items;
+      share = few ? kWarps : share_of(all, gridDim.x);
+      w0 = blockIdx.x * share;
+      if (tid == 0) *head_at<D>(a, blockIdx.x) = make_int4(0, 0, 0, 0);
+    };
+    if (a.c.B <= 32) {                            // every warp scans for itself
+      const int tiles = lane < a.c.B ? span_of(a, lane, bad).tiles : 0;
+      Sums inc = {tiles, rounded(tiles)}, total;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int64_t x = __shfl_up_sync(kAll, inc.tiles, o), y = __shfl_up_sync(kAll, inc.rounded, o);
+        if (lane >= o) { inc.tiles += x; inc.rounded += y; }
+      }
+      total.tiles = __shfl_sync(kAll, inc.tiles, 31);
+      total.rounded = __shfl_sync(kAll, inc.rounded, 31);
+      lay_out(total);
+      const int n = few ? rounded(tiles) : tiles;
+      const int64_t end = (few ? inc.rounded : inc.tiles) * items, begin = end - static_cast<int64_t>(n) * items;
+      const unsigned hit = __ballot_sync(kAll, begin <= w0 && w0 < end);
+      p.b = hit ? __ffs(hit) - 1 : 0;
+      off = w0 - __shfl_sync(kAll, begin, p.b);
+    } else {
+      int b0, b1;
+      Sums total;
+      const Sums before = scan_tiles(a, tid, b0, b1, total, sums, bad);
+      lay_out(total);
+      int64_t at = few ? before.rounded : before.tiles;
+      for (int b = b0; b < b1; ++b) {
+        const int tiles = span_of(a, b, bad).tiles, n = few ? rounded(tiles) : tiles;
+        if (at * items <= w0 && w0 < (at + n) * items) {           // one thread finds it
+          sums[2 * kWarps] = b;
+          sums[2 * kWarps + 1] = w0 - at * items;
+        }
+        at += n;
+      }
+      __syncthreads();
+      p.b = w0 < all ? static_cast<int>(sums[2 * kWarps]) : 0;
+      off = sums[2 * kWarps + 1];
+    }
     if (w0 >= all) {
+      write_empty(a, bad);
       if (bad) atomicOr(&g_decode_fault, bad);
       return;
     }
-    int64_t at = few ? before.rounded : before.tiles;
-    for (int b = b0; b < b1; ++b) {
-      const int tiles = span_of(a, b, bad).tiles, n = few ? rounded(tiles) : tiles;
-      if (at * items <= w0 && w0 < (at + n) * items) {             // one thread finds it
-        sums[2 * kWarps] = b;
-        sums[2 * kWarps + 1] = w0 - at * items;
-      }
-      at += n;
-    }
-    __syncthreads();
-    p.b = static_cast<int>(sums[2 * kWarps]);
-    const int64_t off = sums[2 * kWarps + 1];
     p.s = span_of(a, p.b, bad);
     const int n = few ? rounded(p.s.tiles) : p.s.tiles;
     p.item = static_cast<int>(off / n);
@@ -273,7 +296,8 @@ __global__ void __launch_bounds__(kWarps * 32, kDecodeBlocks<D>) paged_decode_ke
   bool more = p.left > 0;                         // there is one
   int lt = p.ta + warp, at = 32;                  // next tile to load, its place among the 32 looked up
   int id0 = -1, id1 = -1;                         // lane i: the cache blocks of the i-th, per 16 keys
-  float sk0 = 0.0f, sk1 = 0.0f, sv0 = -INFINITY, sv1 = -INFINITY, iv0 = 0.0f, iv1 = 0.0f;   // and S_K, log2 S_V, 1 / S_V
+  float sk0 = 0.0f, sk1 = 0.0f, sv0 = 0.0f, sv1 = 0.0f, iv0 = 0.0f, iv1 = 0.0f;         // and S_K, log2 S_V, 1 / S_V
+  bool fresh = false;                             // S_V as it was loaded
   int lslot = 0, ltiles = 0;
   bool vnext = false;
   int64_t src0 = -1, src1 = -1;                   // the tile's two 16-key parts: this lane's byte offset, or -1
@@ -296,8 +320,8 @@ __global__ void __launch_bounds__(kWarps * 32, kDecodeBlocks<D>) paged_decode_ke
           at = 0;
           const int n = lt + kWarps * lane;
           id0 = id1 = -1;
-          sk0 = sk1 = iv0 = iv1 = 0.0f;
-          sv0 = sv1 = -INFINITY;                  // no block: weights 0
+          sk0 = sk1 = 0.0f;
+          fresh = true;
           if (n < lp.tb) {
             const int key = lp.s.first + n * kTile, j = key >> a.c.log_block;
             // blocks that hold no visible position are not looked up
@@ -307,16 +331,12 @@ __global__ void __launch_bounds__(kWarps * 32, kDecodeBlocks<D>) paged_decode_ke
             if (id0 >= 0) {
               const int64_t x = static_cast<int64_t>(id0) * a.c.Hkv + kvh;
               sk0 = a.c.ks[x];
-              const float v = fmaxf(a.c.vs[x], kScaleMin);
-              sv0 = log2f(v);
-              iv0 = __frcp_rn(v);
+              sv0 = a.c.vs[x];
             }
             if (id1 >= 0) {
               const int64_t x = static_cast<int64_t>(id1) * a.c.Hkv + kvh;
               sk1 = a.c.ks[x];
-              const float v = fmaxf(a.c.vs[x], kScaleMin);
-              sv1 = log2f(v);
-              iv1 = __frcp_rn(v);
+              sv1 = a.c.vs[x];
             }
           }
         }
@@ -350,6 +370,14 @@ __global__ void __launch_bounds__(kWarps * 32, kDecodeBlocks<D>) paged_decode_ke
     }
     copies_commit();
     if (!vnext && more) {
+      if (fresh) {                                // the scales' loads had the copies' issue to arrive in
+        fresh = false;
+        const float v0 = fmaxf(sv0, kScaleMin), v1 = fmaxf(sv1, kScaleMin);
+        sv0 = id0 >= 0 ? log2f(v0) : -INFINITY;   // no block: weights 0
+        sv1 = id1 >= 0 ? log2f(v1) : -INFINITY;
+        iv0 = id0 >= 0 ? __frcp_rn(v0) : 0.0f;
+        iv1 = id1 >= 0 ? __frcp_rn(v1) : 0.0f;
+      }
       if (lane == at) {
         float4* m = my_meta + 2 * (ltiles & (kMetaSlots - 1));
         m[0] = make_float4(sk0, sk1, sv0, sv1);
@@ -606,6 +634,7 @@ __global__ void __launch_bounds__(kWarps * 32, kDecodeBlocks<D>) paged_decode_ke
     any = next_piece(a, p, items, bad);
   }
   copies_wait<0>();
+  if (a.part != nullptr) write_empty(a, bad);
   if (a.part == nullptr && p.s.tiles == 0 && warp == 0) {          // an empty sequence's item
     const int kvh = p.item / groups, h0 = (p.item % groups) * kHeads, heads = min(kHeads, a.R - h0);
     uint16_t* o = a.out + (static_cast<int64_t>(p.b) * a.c.Hkv * a.R + kvh * a.R + h0) * D;
