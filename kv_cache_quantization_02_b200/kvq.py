@@ -488,6 +488,7 @@ def dequantize(packed: torch.Tensor, scales: torch.Tensor, lam: torch.Tensor,
 
 _PAGED_FORMAT = {torch.int8: KVQ_INT8, torch.float8_e4m3fn: KVQ_E4M3}
 _PAGED_DTYPE = {torch.float16: KVQ_FP16, torch.bfloat16: KVQ_BF16}
+_F32, _I32, _U8 = torch.float32, torch.int32, torch.uint8
 
 # torch.cuda.current_device() and the handle of current_stream(index) without
 # the objects around them (a microsecond a call)
@@ -514,25 +515,33 @@ def _paged_cache(block_table, k_cache, v_cache, k_scales, v_scales):
     if index < 0:
         raise ValueError("k_cache must be a CUDA tensor")
     num_blocks, Hkv, block, D = shape
-    _paged_need(k_cache, dtype, shape, index, "k_cache")
-    _paged_need(v_cache, dtype, shape, index, "v_cache")
-    _paged_need(k_scales, torch.float32, (num_blocks, Hkv), index, "k_scales")
-    _paged_need(v_scales, torch.float32, (num_blocks, Hkv), index, "v_scales")
     B, max_blocks = block_table.shape
-    _paged_need(block_table, torch.int32, (B, max_blocks), index, "block_table")
+    one = (num_blocks, Hkv)
+    if not (v_cache.dtype is dtype and v_cache.shape == shape and k_scales.dtype is _F32 and k_scales.shape == one
+            and v_scales.dtype is _F32 and v_scales.shape == one and block_table.dtype is _I32
+            and k_cache.is_contiguous() and v_cache.is_contiguous() and k_scales.is_contiguous()
+            and v_scales.is_contiguous() and block_table.is_contiguous()
+            and v_cache.get_device() == k_scales.get_device() == v_scales.get_device()
+            == block_table.get_device() == index):
+        _paged_need(k_cache, dtype, shape, index, "k_cache")
+        _paged_need(v_cache, dtype, shape, index, "v_cache")
+        _paged_need(k_scales, _F32, one, index, "k_scales")
+        _paged_need(v_scales, _F32, one, index, "v_scales")
+        _paged_need(block_table, _I32, (B, max_blocks), index, "block_table")
     return index, fmt, B, max_blocks, num_blocks, Hkv, block, D
 
 
 def _paged_rows(x, name, D, index):
     """Checks token rows [n, heads, D] that may lie apart; (element type, n, heads, stride)."""
-    if x.dim() != 3 or x.shape[2] != D:
-        raise ValueError(f"{name} must be [tokens, heads, {D}], got {tuple(x.shape)}")
     dtype = _PAGED_DTYPE.get(x.dtype)
     if dtype is None:
         raise ValueError(f"{name} must be torch.float16 or torch.bfloat16, got {x.dtype}")
+    shape = x.shape
+    if len(shape) != 3 or shape[2] != D:
+        raise ValueError(f"{name} must be [tokens, heads, {D}], got {tuple(shape)}")
     if x.get_device() != index:
         raise ValueError(f"{name} must be on cuda:{index} as the cache, got {x.device}")
-    n, heads, _ = x.shape
+    n, heads, _ = shape
     s0, s1, s2 = x.stride()
     if s2 != 1 or (s1 != D and heads > 1):
         raise ValueError(f"{name}: the channels and heads of a token must be contiguous")
@@ -581,8 +590,8 @@ def paged_write(k: torch.Tensor, v: torch.Tensor, cu_tokens: torch.Tensor, start
     if heads != Hkv or v_heads != Hkv or v_n != n or v_dtype != dtype:
         raise ValueError(f"k and v must both be [n, {Hkv}, {D}] of one type, "
                          f"got {tuple(k.shape)} {k.dtype} and {tuple(v.shape)} {v.dtype}")
-    _paged_need(cu_tokens, torch.int32, (B + 1,), index, "cu_tokens")
-    _paged_need(start, torch.int32, (B,), index, "start")
+    _paged_need(cu_tokens, _I32, (B + 1,), index, "cu_tokens")
+    _paged_need(start, _I32, (B,), index, "start")
     _paged_call(index, _lib.kvq_paged_write, k.data_ptr(), v.data_ptr(), dtype, k_stride, v_stride,
                 cu_tokens.data_ptr(), start.data_ptr(), block_table.data_ptr(), B, max_blocks, n, Hkv, D, block, fmt,
                 num_blocks, k_cache.data_ptr(), v_cache.data_ptr(), k_scales.data_ptr(), v_scales.data_ptr(),
@@ -603,8 +612,8 @@ def paged_read(cu_tokens: torch.Tensor, start: torch.Tensor, block_table: torch.
     code = _PAGED_DTYPE.get(dtype)
     if code is None:
         raise ValueError(f"dtype must be torch.float16 or torch.bfloat16, got {dtype}")
-    _paged_need(cu_tokens, torch.int32, (B + 1,), index, "cu_tokens")
-    _paged_need(start, torch.int32, (B,), index, "start")
+    _paged_need(cu_tokens, _I32, (B + 1,), index, "cu_tokens")
+    _paged_need(start, _I32, (B,), index, "start")
     shape = (n_tokens, Hkv, D)
     if k_out is None:
         k_out = torch.empty(shape, dtype=dtype, device=k_cache.device)
@@ -633,11 +642,11 @@ def _paged_workspace(workspace, like, index, *shape):
         need = _paged_workspace_bytes(index, *shape)
         if need <= 0:
             return None, 0, 0
-        workspace = like.new_empty(need, dtype=torch.uint8)
+        workspace = like.new_empty(need, dtype=_U8)
         return workspace, workspace.data_ptr(), need
     if not isinstance(workspace, torch.Tensor):
         return None, 0, 0
-    _paged_need(workspace, torch.uint8, (workspace.numel(),), index, "workspace")
+    _paged_need(workspace, _U8, (workspace.numel(),), index, "workspace")
     return workspace, workspace.data_ptr(), workspace.numel()
 
 
@@ -658,7 +667,7 @@ def paged_attention_decode(q: torch.Tensor, seq_len: torch.Tensor, block_table: 
     dtype, n, Hq, q_stride = _paged_rows(q, "q", D, index)
     if n != B:
         raise ValueError(f"q must have one row for each of the {B} sequences, got {n}")
-    _paged_need(seq_len, torch.int32, (B,), index, "seq_len")
+    _paged_need(seq_len, _I32, (B,), index, "seq_len")
     if out is None:
         out = q.new_empty((B, Hq, D))
     else:
@@ -686,8 +695,8 @@ def paged_attention_prefill(q: torch.Tensor, cu_q: torch.Tensor, seq_len: torch.
     index, fmt, B, max_blocks, num_blocks, Hkv, block, D = _paged_cache(block_table, k_cache, v_cache, k_scales,
                                                                         v_scales)
     dtype, n, Hq, q_stride = _paged_rows(q, "q", D, index)
-    _paged_need(cu_q, torch.int32, (B + 1,), index, "cu_q")
-    _paged_need(seq_len, torch.int32, (B,), index, "seq_len")
+    _paged_need(cu_q, _I32, (B + 1,), index, "cu_q")
+    _paged_need(seq_len, _I32, (B,), index, "seq_len")
     if out is None:
         out = q.new_empty((n, Hq, D))
     else:
