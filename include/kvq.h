@@ -409,9 +409,9 @@ int kvq_paged_read(const int32_t *cu_tokens, const int32_t *start, const int32_t
  *   seq_len     [in]  int32 [B], each in [0, max_blocks * block].
  *   out         [out] [B][Hq][D], contiguous; must not overlap the inputs.
  *   workspace   scratch for splitting the key axis; 16-byte aligned, at least
- *               kvq_paged_workspace_bytes().  With less, or NULL, the call
- *               runs unsplit: same result up to fp32 summation order, slower.
- *               Calls that may overlap in time need one each.
+ *               kvq_paged_decode_workspace_bytes().  With less, or NULL, the
+ *               call runs unsplit: same result up to fp32 summation order,
+ *               slower.  Calls that may overlap in time need one each.
  * The codes enter the products exactly, scores and sums are fp32, the softmax
  * weights are fp16 values (relative rounding 2^-11) in the value product.
  * Scales are read as max(scale, 2^-40).
@@ -433,7 +433,8 @@ int kvq_paged_attention_decode(const void *q, int dtype, int64_t q_stride, const
  *   q     [in]  [total_q][Hq][D], tokens q_stride apart.
  *   cu_q  [in]  int32 [B + 1], from 0, not decreasing.
  *   out   [out] [total_q][Hq][D], contiguous; must not overlap the inputs.
- * Other arguments and numerics as for kvq_paged_attention_decode.
+ * Other arguments and numerics as for kvq_paged_attention_decode, with
+ * kvq_paged_prefill_workspace_bytes() of workspace.
  */
 int kvq_paged_attention_prefill(const void *q, int dtype, int64_t q_stride, const int32_t *cu_q,
                                 const int32_t *seq_len, const int32_t *block_table, int B,
@@ -444,12 +445,14 @@ int kvq_paged_attention_prefill(const void *q, int dtype, int64_t q_stride, cons
                                 int64_t workspace_bytes, void *stream);
 
 /*
- * kvq_paged_workspace_bytes -- bytes of workspace that kvq_paged_attention_decode
- * (total_q = B) or kvq_paged_attention_prefill uses for these shapes on the
- * current device, or -1 if the shapes are invalid.  Host-only.
+ * kvq_paged_decode_workspace_bytes, kvq_paged_prefill_workspace_bytes -- bytes
+ * of workspace that the two calls use for these shapes on the current device (0:
+ * they do not split), or -1 if the shapes are invalid.  Host-only.
  */
-int64_t kvq_paged_workspace_bytes(int B, int max_blocks, int64_t total_q, int Hq, int Hkv, int D,
-                                  int block);
+int64_t kvq_paged_decode_workspace_bytes(int B, int max_blocks, int Hq, int Hkv, int D, int block,
+                                         int window);
+int64_t kvq_paged_prefill_workspace_bytes(int B, int max_blocks, int64_t total_q, int Hq, int Hkv,
+                                          int D, int block, int window);
 
 /*
  * kvq_fault_status -- the current device's fault word: 0 when every bounded

@@ -329,11 +329,14 @@ int sm_count() {
 }
 
 // Thread blocks of a split decode call: all that the GPU holds at once, or one
-// per four tiles of 32 keys if the table has room, or the window, for fewer.
+// per four tiles of 32 keys if the table has room, or the window, for fewer.  0:
+// up to eight tiles, two a warp, are one thread block's, which saves the second
+// kernel (about 2 us, as much as six more tiles).
 int decode_grid(int B, int max_blocks, int Hq, int Hkv, int D, int block, int window) {
   const int64_t items = static_cast<int64_t>(B) * Hkv * ((Hq / Hkv + 7) / 8);
   int64_t tiles = (static_cast<int64_t>(max_blocks) * block + 31) / 32 + 1;
   if (window > 0 && window / 32 + 2 < tiles) tiles = window / 32 + 2;
+  if (tiles <= 8) return 0;
   const int64_t full = static_cast<int64_t>(sm_count()) *
                        (D == 64 ? kDecodeBlocks<64> : D == 128 ? kDecodeBlocks<128> : kDecodeBlocks<256>);
   if (items >= full) return static_cast<int>(full);
@@ -528,12 +531,23 @@ int kvq_paged_read(const int32_t* cu_tokens, const int32_t* start, const int32_t
   return finish();
 }
 
-int64_t kvq_paged_workspace_bytes(int B, int max_blocks, int64_t total_q, int Hq, int Hkv, int D, int block) {
-  if (check_shape(KVQ_FP16, KVQ_INT8, B, max_blocks, Hkv, D, block, 0) != KVQ_OK) return -1;
-  if (Hq < Hkv || Hq % Hkv != 0 || total_q < 0 || total_q > INT32_MAX || total_q * Hq > INT32_MAX) return -1;
-  const int64_t one = decode_bytes(decode_grid(B, max_blocks, Hq, Hkv, D, block, 0), D);
-  const int64_t many = prompt_grid(B, max_blocks, total_q, Hq, Hkv, D, block, 0).bytes;
-  return one > many ? one : many;
+static int check_workspace(int B, int max_blocks, int64_t total_q, int Hq, int Hkv, int D, int block, int window) {
+  const int rc = check_shape(KVQ_FP16, KVQ_INT8, B, max_blocks, Hkv, D, block, 0);
+  if (rc != KVQ_OK) return rc;
+  return Hq < Hkv || Hq % Hkv != 0 || total_q < 0 || total_q > INT32_MAX || total_q * Hq > INT32_MAX || window < 0
+             ? KVQ_ERR_COUNT
+             : KVQ_OK;
+}
+
+int64_t kvq_paged_decode_workspace_bytes(int B, int max_blocks, int Hq, int Hkv, int D, int block, int window) {
+  if (check_workspace(B, max_blocks, B, Hq, Hkv, D, block, window) != KVQ_OK) return -1;
+  return decode_bytes(decode_grid(B, max_blocks, Hq, Hkv, D, block, window), D);
+}
+
+int64_t kvq_paged_prefill_workspace_bytes(int B, int max_blocks, int64_t total_q, int Hq, int Hkv, int D, int block,
+                                          int window) {
+  if (check_workspace(B, max_blocks, total_q, Hq, Hkv, D, block, window) != KVQ_OK) return -1;
+  return prompt_grid(B, max_blocks, total_q, Hq, Hkv, D, block, window).bytes;
 }
 
 int kvq_paged_attention_decode(const void* q, int dtype, int64_t q_stride, const int32_t* seq_len,

@@ -71,8 +71,10 @@ _lib.kvq_paged_attention_decode.argtypes = [_P, _I, _I64, _P, _P, _I, _I, _I, _I
 _lib.kvq_paged_attention_prefill.restype = _I
 _lib.kvq_paged_attention_prefill.argtypes = [_P, _I, _I64, _P, _P, _P, _I, _I, _I64, _I, _I, _I, _I, _I, _I64,
                                              _P, _P, _P, _P, ctypes.c_float, _I, _P, _P, _I64, _P]
-_lib.kvq_paged_workspace_bytes.restype = _I64
-_lib.kvq_paged_workspace_bytes.argtypes = [_I, _I, _I64, _I, _I, _I, _I]
+_lib.kvq_paged_decode_workspace_bytes.restype = _I64
+_lib.kvq_paged_decode_workspace_bytes.argtypes = [_I, _I, _I, _I, _I, _I, _I]
+_lib.kvq_paged_prefill_workspace_bytes.restype = _I64
+_lib.kvq_paged_prefill_workspace_bytes.argtypes = [_I, _I, _I64, _I, _I, _I, _I, _I]
 _lib.kvq_status_string.restype = ctypes.c_char_p
 _lib.kvq_status_string.argtypes = [_I]
 _lib.kvq_last_cuda_error.restype = _I
@@ -230,8 +232,14 @@ def kvq_paged_attention_prefill(q: int, dtype: int, q_stride: int, cu_q: int, se
                                             v_scales, sm_scale, window, out, workspace, workspace_bytes, stream)
 
 
-def kvq_paged_workspace_bytes(B: int, max_blocks: int, total_q: int, Hq: int, Hkv: int, D: int, block: int) -> int:
-    return _lib.kvq_paged_workspace_bytes(B, max_blocks, total_q, Hq, Hkv, D, block)
+def kvq_paged_decode_workspace_bytes(B: int, max_blocks: int, Hq: int, Hkv: int, D: int, block: int,
+                                     window: int = 0) -> int:
+    return _lib.kvq_paged_decode_workspace_bytes(B, max_blocks, Hq, Hkv, D, block, window)
+
+
+def kvq_paged_prefill_workspace_bytes(B: int, max_blocks: int, total_q: int, Hq: int, Hkv: int, D: int, block: int,
+                                      window: int = 0) -> int:
+    return _lib.kvq_paged_prefill_workspace_bytes(B, max_blocks, total_q, Hq, Hkv, D, block, window)
 
 
 def kvq_status_string(status: int) -> str:
@@ -531,6 +539,14 @@ def _paged_cache(block_table, k_cache, v_cache, k_scales, v_scales):
     return index, fmt, B, max_blocks, num_blocks, Hkv, block, D
 
 
+def _paged_lists(cu, cu_name, each, each_name, B, index):
+    """Checks offsets [B + 1] and a list [B], int32."""
+    if not (cu.dtype is _I32 and each.dtype is _I32 and cu.shape == (B + 1,) and each.shape == (B,)
+            and cu.is_contiguous() and each.is_contiguous() and cu.get_device() == each.get_device() == index):
+        _paged_need(cu, _I32, (B + 1,), index, cu_name)
+        _paged_need(each, _I32, (B,), index, each_name)
+
+
 def _paged_rows(x, name, D, index):
     """Checks token rows [n, heads, D] that may lie apart; (element type, n, heads, stride)."""
     dtype = _PAGED_DTYPE.get(x.dtype)
@@ -590,8 +606,7 @@ def paged_write(k: torch.Tensor, v: torch.Tensor, cu_tokens: torch.Tensor, start
     if heads != Hkv or v_heads != Hkv or v_n != n or v_dtype != dtype:
         raise ValueError(f"k and v must both be [n, {Hkv}, {D}] of one type, "
                          f"got {tuple(k.shape)} {k.dtype} and {tuple(v.shape)} {v.dtype}")
-    _paged_need(cu_tokens, _I32, (B + 1,), index, "cu_tokens")
-    _paged_need(start, _I32, (B,), index, "start")
+    _paged_lists(cu_tokens, "cu_tokens", start, "start", B, index)
     _paged_call(index, _lib.kvq_paged_write, k.data_ptr(), v.data_ptr(), dtype, k_stride, v_stride,
                 cu_tokens.data_ptr(), start.data_ptr(), block_table.data_ptr(), B, max_blocks, n, Hkv, D, block, fmt,
                 num_blocks, k_cache.data_ptr(), v_cache.data_ptr(), k_scales.data_ptr(), v_scales.data_ptr(),
@@ -612,15 +627,14 @@ def paged_read(cu_tokens: torch.Tensor, start: torch.Tensor, block_table: torch.
     code = _PAGED_DTYPE.get(dtype)
     if code is None:
         raise ValueError(f"dtype must be torch.float16 or torch.bfloat16, got {dtype}")
-    _paged_need(cu_tokens, _I32, (B + 1,), index, "cu_tokens")
-    _paged_need(start, _I32, (B,), index, "start")
+    _paged_lists(cu_tokens, "cu_tokens", start, "start", B, index)
     shape = (n_tokens, Hkv, D)
     if k_out is None:
-        k_out = torch.empty(shape, dtype=dtype, device=k_cache.device)
+        k_out = k_cache.new_empty(shape, dtype=dtype)
     else:
         _paged_need(k_out, dtype, shape, index, "k_out")
     if v_out is None:
-        v_out = torch.empty(shape, dtype=dtype, device=k_cache.device)
+        v_out = k_cache.new_empty(shape, dtype=dtype)
     else:
         _paged_need(v_out, dtype, shape, index, "v_out")
     _paged_call(index, _lib.kvq_paged_read, cu_tokens.data_ptr(), start.data_ptr(), block_table.data_ptr(), B,
@@ -631,15 +645,15 @@ def paged_read(cu_tokens: torch.Tensor, start: torch.Tensor, block_table: torch.
 
 
 @functools.lru_cache(maxsize=4096)
-def _paged_workspace_bytes(index, *shape):
+def _paged_workspace_bytes(size, index, *shape):
     with torch.cuda.device(index):
-        return _lib.kvq_paged_workspace_bytes(*shape)
+        return size(*shape)
 
 
-def _paged_workspace(workspace, like, index, *shape):
+def _paged_workspace(workspace, like, size, index, *shape):
     """(tensor or None, address, bytes): `workspace` True allocates what the library asks for."""
     if workspace is True:
-        need = _paged_workspace_bytes(index, *shape)
+        need = _paged_workspace_bytes(size, index, *shape)
         if need <= 0:
             return None, 0, 0
         workspace = like.new_empty(need, dtype=_U8)
@@ -672,7 +686,8 @@ def paged_attention_decode(q: torch.Tensor, seq_len: torch.Tensor, block_table: 
         out = q.new_empty((B, Hq, D))
     else:
         _paged_need(out, q.dtype, (B, Hq, D), index, "out")
-    ws, ws_ptr, ws_bytes = _paged_workspace(workspace, q, index, B, max_blocks, B, Hq, Hkv, D, block)
+    ws, ws_ptr, ws_bytes = _paged_workspace(workspace, q, kvq_paged_decode_workspace_bytes, index, B, max_blocks, Hq, Hkv,
+                                            D, block, window)
     _paged_call(index, _lib.kvq_paged_attention_decode, q.data_ptr(), dtype, q_stride, seq_len.data_ptr(),
                 block_table.data_ptr(), B, max_blocks, Hq, Hkv, D, block, fmt, num_blocks, k_cache.data_ptr(),
                 v_cache.data_ptr(), k_scales.data_ptr(), v_scales.data_ptr(), sm_scale, window, out.data_ptr(), ws_ptr,
@@ -695,13 +710,13 @@ def paged_attention_prefill(q: torch.Tensor, cu_q: torch.Tensor, seq_len: torch.
     index, fmt, B, max_blocks, num_blocks, Hkv, block, D = _paged_cache(block_table, k_cache, v_cache, k_scales,
                                                                         v_scales)
     dtype, n, Hq, q_stride = _paged_rows(q, "q", D, index)
-    _paged_need(cu_q, _I32, (B + 1,), index, "cu_q")
-    _paged_need(seq_len, _I32, (B,), index, "seq_len")
+    _paged_lists(cu_q, "cu_q", seq_len, "seq_len", B, index)
     if out is None:
         out = q.new_empty((n, Hq, D))
     else:
         _paged_need(out, q.dtype, (n, Hq, D), index, "out")
-    ws, ws_ptr, ws_bytes = _paged_workspace(workspace, q, index, B, max_blocks, n, Hq, Hkv, D, block)
+    ws, ws_ptr, ws_bytes = _paged_workspace(workspace, q, kvq_paged_prefill_workspace_bytes, index, B, max_blocks, n, Hq,
+                                            Hkv, D, block, window)
     _paged_call(index, _lib.kvq_paged_attention_prefill, q.data_ptr(), dtype, q_stride, cu_q.data_ptr(),
                 seq_len.data_ptr(), block_table.data_ptr(), B, max_blocks, n, Hq, Hkv, D, block, fmt, num_blocks,
                 k_cache.data_ptr(), v_cache.data_ptr(), k_scales.data_ptr(), v_scales.data_ptr(), sm_scale, window,

@@ -107,11 +107,14 @@ def test_attention(kvq):
 
 
 def test_workspace_shapes(kvq):
-    ok = dict(B=4, max_blocks=64, total_q=4, Hq=32, Hkv=8, D=128, block=64)
-    f = lambda **kw: kvq.kvq_paged_workspace_bytes(*dict(ok, **kw).values())
-    assert f() >= 0
-    for kw in (dict(D=96), dict(block=8), dict(Hq=30), dict(Hkv=0), dict(total_q=-1), dict(B=-1)):
-        assert f(**kw) == -1
+    ok = dict(B=4, max_blocks=64, Hq=32, Hkv=8, D=128, block=64, window=0)
+    f = lambda **kw: kvq.kvq_paged_decode_workspace_bytes(**dict(ok, **kw))
+    g = lambda **kw: kvq.kvq_paged_prefill_workspace_bytes(**dict(ok, total_q=40, **kw))
+    assert f() > 0 and g() >= 0
+    assert f(max_blocks=2) == 0 and f(window=100) == 0            # little to split
+    for kw in (dict(D=96), dict(block=8), dict(Hq=30), dict(Hkv=0), dict(B=-1), dict(window=-1)):
+        assert f(**kw) == -1 and g(**kw) == -1
+    assert kvq.kvq_paged_prefill_workspace_bytes(4, 64, -1, 32, 8, 128, 64) == -1
     assert kvq.kvq_status_string(-7).startswith("KVQ_ERR_FORMAT")
 
 
