@@ -177,14 +177,14 @@ struct Job {
 template <int D>
 __device__ __forceinline__ bool find_job(const AttnArgs& a, int nsplit, Job& j, unsigned& bad) {
   using C = Prefill<D>;
-  int64_t x = blockIdx.x;
-  j.split = static_cast<int>(x % nsplit);
-  x /= nsplit;
+  unsigned x = blockIdx.x;
+  j.split = static_cast<int>(x % static_cast<unsigned>(nsplit));
+  x /= static_cast<unsigned>(nsplit);
   j.tile = x;
-  j.kvh = static_cast<int>(x % a.c.Hkv);
+  j.kvh = static_cast<int>(x % static_cast<unsigned>(a.c.Hkv));
   // the last tiles of a sequence see most keys: they start first
-  const int64_t items = a.total_q * a.R / C::ROWS + a.c.B;
-  const int64_t item = items - 1 - x / a.c.Hkv;
+  const int64_t items = (a.total_q * a.R >> C::LOG_ROWS) + a.c.B;
+  const int64_t item = items - 1 - x / static_cast<unsigned>(a.c.Hkv);
   const Found f = find_sequence(a.cu, a.seq_len, a.c.B, item, a.R, C::LOG_ROWS, 1, threadIdx.x & 31);
   j.b = f.b;
   const int64_t k = f.item, c0 = f.c0, c1 = f.c1;
@@ -204,8 +204,9 @@ __device__ __forceinline__ bool find_job(const AttnArgs& a, int nsplit, Job& j, 
   j.hi = max(0, p1 + 1);
   j.first = j.lo / C::KT * C::KT;
   const int tiles = j.hi > j.lo ? (j.hi - j.first + C::KT - 1) / C::KT : 0;
-  const int t0 = static_cast<int>(static_cast<int64_t>(tiles) * j.split / nsplit);
-  const int t1 = static_cast<int>(static_cast<int64_t>(tiles) * (j.split + 1) / nsplit);
+  // (tiles < 2^25 and nsplit <= 16)
+  const int t0 = static_cast<int>(static_cast<unsigned>(tiles * j.split) / static_cast<unsigned>(nsplit));
+  const int t1 = static_cast<int>(static_cast<unsigned>(tiles * (j.split + 1)) / static_cast<unsigned>(nsplit));
   j.first += t0 * C::KT;
   j.tiles = t1 - t0;
   j.steps = j.tiles > 0 ? min(j.tiles * C::STEPS, (j.hi - j.first + kStep - 1) / kStep) : 0;
@@ -295,10 +296,11 @@ __global__ void __launch_bounds__(kThreads, 1) paged_prefill_kernel(AttnArgs a, 
                  :: "r"(smem_addr(shared_word)), "n"(C::COLS) : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
+  const int sets = C::MT == 2 && j.count > 128 ? 2 : 1;     // of 128 rows: an empty second one is left out
   if (tid == 0) {
     for (int i = 0; i < ST; ++i) {
       mbar_init(&k_full[i], 4); mbar_init(&v_full[i], 4);
-      mbar_init(&k_empty[i], C::MT); mbar_init(&v_empty[i], C::MT);
+      mbar_init(&k_empty[i], sets); mbar_init(&v_empty[i], sets);
     }
     for (int i = 0; i < 4; ++i) mbar_init(&meta_full[i], 1);
     // per 128 rows, steps alternate between two of each: a wait is then never two
@@ -367,7 +369,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_prefill_kernel(AttnArgs a, 
     // ---- softmax
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" :: "n"(kSoftmaxRegs));
     const int mt = warp >> 2;
-    if (mt < C::MT) {
+    if (mt < sets) {
       const int r = mt * 128 + (warp & 3) * 32 + lane;
       const uint32_t lanes = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
       const uint32_t o_at = lanes + C::O0 + mt * D;
@@ -531,7 +533,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_prefill_kernel(AttnArgs a, 
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" :: "n"(kIssuerRegs));
     {
       // ---- the MMAs
-      if (warp < kIssuer + C::MT && j.tiles > 0) {
+      if (warp < kIssuer + sets && j.tiles > 0) {
         const int mt = warp - kIssuer;
         constexpr uint32_t sdesc = kMmaDesc<kStep, false>, odesc = kMmaDesc<D, true>;
         const uint32_t one = elect_one();
