@@ -682,6 +682,7 @@ def paged_attention_decode(q: torch.Tensor, seq_len: torch.Tensor, block_table: 
     if n != B:
         raise ValueError(f"q must have one row for each of the {B} sequences, got {n}")
     _paged_need(seq_len, _I32, (B,), index, "seq_len")
+    window = int(window)
     if out is None:
         out = q.new_empty((B, Hq, D))
     else:
@@ -690,8 +691,8 @@ def paged_attention_decode(q: torch.Tensor, seq_len: torch.Tensor, block_table: 
                                             D, block, window)
     _paged_call(index, _lib.kvq_paged_attention_decode, q.data_ptr(), dtype, q_stride, seq_len.data_ptr(),
                 block_table.data_ptr(), B, max_blocks, Hq, Hkv, D, block, fmt, num_blocks, k_cache.data_ptr(),
-                v_cache.data_ptr(), k_scales.data_ptr(), v_scales.data_ptr(), sm_scale, window, out.data_ptr(), ws_ptr,
-                ws_bytes, _current_stream(index))
+                v_cache.data_ptr(), k_scales.data_ptr(), v_scales.data_ptr(), float(sm_scale), window, out.data_ptr(),
+                ws_ptr, ws_bytes, _current_stream(index))
     return out
 
 
@@ -703,7 +704,8 @@ def paged_attention_prefill(q: torch.Tensor, cu_q: torch.Tensor, seq_len: torch.
     """Causal attention of any number of new tokens per sequence.  q fp16 or
     bf16 [n, Hq, D], sequence b's in rows cu_q[b] .. cu_q[b + 1] (int32
     [B + 1]), the last of them at position seq_len[b] - 1; the rest as for
-    paged_attention_decode -> [n, Hq, D]."""
+    paged_attention_decode -> [n, Hq, D].  Rows from cu_q[B] on are not
+    written."""
     if stream is not None:
         return _on_stream(paged_attention_prefill, stream, k_cache.get_device(), q, cu_q, seq_len, block_table,
                           k_cache, v_cache, k_scales, v_scales, sm_scale, window, out, workspace)
@@ -711,6 +713,7 @@ def paged_attention_prefill(q: torch.Tensor, cu_q: torch.Tensor, seq_len: torch.
                                                                         v_scales)
     dtype, n, Hq, q_stride = _paged_rows(q, "q", D, index)
     _paged_lists(cu_q, "cu_q", seq_len, "seq_len", B, index)
+    window = int(window)
     if out is None:
         out = q.new_empty((n, Hq, D))
     else:
@@ -719,6 +722,6 @@ def paged_attention_prefill(q: torch.Tensor, cu_q: torch.Tensor, seq_len: torch.
                                             Hkv, D, block, window)
     _paged_call(index, _lib.kvq_paged_attention_prefill, q.data_ptr(), dtype, q_stride, cu_q.data_ptr(),
                 seq_len.data_ptr(), block_table.data_ptr(), B, max_blocks, n, Hq, Hkv, D, block, fmt, num_blocks,
-                k_cache.data_ptr(), v_cache.data_ptr(), k_scales.data_ptr(), v_scales.data_ptr(), sm_scale, window,
+                k_cache.data_ptr(), v_cache.data_ptr(), k_scales.data_ptr(), v_scales.data_ptr(), float(sm_scale), window,
                 out.data_ptr(), ws_ptr, ws_bytes, _current_stream(index))
     return out

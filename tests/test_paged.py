@@ -46,6 +46,7 @@ WRITES = [
     (256, 2, 16, "e4m3", "bf16", [0, 3, 500], [16, 1, 31]),
     (256, 1, 64, "int8", "bf16", [10] * 40, [1] * 39 + [0]),
     (64, 5, 32, "int8", "bf16", list(range(70)), [3] * 70),
+    (128, 2, 32, "e4m3", "fp16", [0, 9, 31] + [4] * 27, [50, 0, 3] + [0] * 27),       # few tokens, most of them one's
 ]
 
 
@@ -316,6 +317,135 @@ def test_zero_values(kvq):
     check(kvq.paged_attention_prefill(q.cuda(), d.cu, d.seq_len, d.table, *d.cache(), sm_scale=0.1), want, bound)
     want, bound = c.attend(q[:1], range(2), c.seq_len, 0.1)
     check(kvq.paged_attention_decode(q[:1].cuda(), d.seq_len, d.table, *d.cache(), sm_scale=0.1), want, bound)
+
+
+@pytest.mark.parametrize("D,block", [(64, 64), (128, 16), (256, 32)])
+@pytest.mark.parametrize("up", [60, -60])
+def test_queries_far_from_one(kvq, D, block, up):
+    """bf16 queries around 2^60 and 2^-60, the softmax scale around 2^-60 and 2^60: beyond fp16, which holds the rows."""
+    c = Case(D, 1, block, "int8", [0, 40], [100, 30], seed=21, R=2)
+    q = (c.rows(2, "bf16").float() * 2.0 ** up).bfloat16()
+    d = c.cuda()
+    scale = 2.0 ** -up / math.sqrt(D)
+    want, bound = c.attend(q, c.cu, c.seq_len, scale)
+    check(kvq.paged_attention_prefill(q.cuda(), d.cu, d.seq_len, d.table, *d.cache(), sm_scale=scale), want, bound)
+    want, bound = c.attend(q[:2], range(3), c.seq_len, scale)
+    check(kvq.paged_attention_decode(q[:2].cuda(), d.seq_len, d.table, *d.cache(), sm_scale=scale), want, bound)
+
+
+@pytest.mark.parametrize("D,block,fmt", [(128, 16, "e4m3"), (128, 64, "int8"), (64, 32, "int8"), (256, 128, "e4m3")])
+@pytest.mark.parametrize("window", [1, 17, 64, 130])
+def test_blocks_before_the_window(kvq, D, block, fmt, window):
+    """Blocks that lie wholly before every window are given up: their table entries may be anything, and none is reported."""
+    c = Case(D, 1, block, fmt, [700, 300, 0], [20, 1, 3], seed=22, R=4)
+    for b in range(3):
+        first = max(0, c.ctx[b] - window + 1) // block               # the first block that a new token sees
+        c.table[b, :first] = -1 if b == 0 else 2 ** 30
+    q = c.rows(4, "bf16")
+    d = c.cuda()
+    want, bound = c.attend(q, c.cu, c.seq_len, 0.2, window)
+    check(kvq.paged_attention_prefill(q.cuda(), d.cu, d.seq_len, d.table, *d.cache(), sm_scale=0.2, window=window),
+          want, bound)
+    last = q[(c.cu[1:] - 1).long()]
+    want, bound = c.attend(last, range(4), c.seq_len, 0.2, window)
+    check(kvq.paged_attention_decode(last.cuda(), d.seq_len, d.table, *d.cache(), sm_scale=0.2, window=window),
+          want, bound)
+
+
+@pytest.mark.parametrize("B", [33, 128, 129, 300])
+def test_many_sequences(kvq, B):
+    """Searches and scans over more sequences than a warp, or a block, looks at at once; empty ones among them."""
+    D, Hkv, block = 64, 2, 16
+    new = [(7 * b) % 5 for b in range(B)]
+    new[B // 2] = 40
+    c = Case(D, Hkv, block, "int8", [(5 * b) % 19 for b in range(B)], new, seed=B, R=2)
+    d = c.cuda()
+    k, v, q = c.rows(Hkv, "fp16"), c.rows(Hkv, "fp16"), c.rows(2 * Hkv, "fp16")
+    kvq.paged_write(k.cuda(), v.cuda(), d.cu, d.start, d.table, *d.cache())
+    c.write(k, v)
+    assert same_cache(c, d)
+    for got, want in zip(kvq.paged_read(d.cu, d.start, d.table, *d.cache(), n_tokens=c.n), c.read("fp16")):
+        assert same(got, want)
+    want, bound = c.attend(q, c.cu, c.seq_len, 0.1)
+    check(kvq.paged_attention_prefill(q.cuda(), d.cu, d.seq_len, d.table, *d.cache(), sm_scale=0.1), want, bound)
+    one = (torch.randn((B, 2 * Hkv, D), generator=c.g)).half()
+    want, bound = c.attend(one, range(B + 1), c.seq_len, 0.1)
+    check(kvq.paged_attention_decode(one.cuda(), d.seq_len, d.table, *d.cache(), sm_scale=0.1), want, bound)
+
+
+def test_thousands_of_sequences(kvq):
+    """4500 sequences in one call are what they are in calls of 30."""
+    B, D, Hkv, block = 4500, 64, 1, 16
+    new = [(3 * b) % 4 for b in range(B)]
+    c = Case(D, Hkv, block, "e4m3", [(11 * b) % 37 for b in range(B)], new, seed=23, R=2)
+    k, v, q = c.rows(Hkv, "bf16").cuda(), c.rows(Hkv, "bf16").cuda(), c.rows(2, "bf16").cuda()
+    d, e = c.cuda(), c.cuda()
+    e.kc, e.vc, e.ks, e.vs = (x.clone() for x in d.cache())
+    kvq.paged_write(k, v, d.cu, d.start, d.table, *d.cache())
+    pieces = [(b, min(B, b + 30)) for b in range(0, B, 30)]
+    part = lambda x, b0, b1: x[int(c.cu[b0]):int(c.cu[b1])]
+    cus = [(d.cu[b0:b1 + 1] - d.cu[b0]).contiguous() for b0, b1 in pieces]
+    for (b0, b1), cu in zip(pieces, cus):
+        kvq.paged_write(part(k, b0, b1), part(v, b0, b1), cu, e.start[b0:b1], e.table[b0:b1], *e.cache())
+    assert same_cache(d, e)
+    out = kvq.paged_attention_prefill(q, d.cu, d.seq_len, d.table, *d.cache(), sm_scale=0.2, workspace=False)
+    one = torch.randn((B, 2, D), generator=c.g).bfloat16().cuda()
+    dec = kvq.paged_attention_decode(one, d.seq_len, d.table, *d.cache(), sm_scale=0.2, workspace=False)
+    for (b0, b1), cu in zip(pieces, cus):
+        lens, table = d.seq_len[b0:b1], d.table[b0:b1]
+        assert same(part(out, b0, b1), kvq.paged_attention_prefill(part(q, b0, b1), cu, lens, table, *d.cache(),
+                                                                   sm_scale=0.2, workspace=False))
+        assert same(dec[b0:b1], kvq.paged_attention_decode(one[b0:b1], lens, table, *d.cache(), sm_scale=0.2,
+                                                           workspace=False))
+    c.kc, c.vc, c.ks, c.vs = (x.cpu() for x in d.cache())
+    want, bound = c.attend(one.cpu(), range(B + 1), c.seq_len, 0.2)
+    check(kvq.paged_attention_decode(one, d.seq_len, d.table, *d.cache(), sm_scale=0.2), want, bound)
+
+
+def test_positions_behind_the_table(kvq):
+    """New tokens that the table has no block for are reported and left out, the others written."""
+    c = Case(128, 1, 16, "int8", [10, 0], [20, 40], seed=24, extra=0)
+    c.table = c.table[:, :2].contiguous()
+    d = c.cuda()
+    k = c.rows(1, "fp16")
+    kvq.paged_write(k.cuda(), k.cuda(), d.cu, d.start, d.table, *d.cache())
+    assert kvq.kvq_fault_status(clear=True) == 4
+    c.write(k, k)
+    assert same_cache(c, d)
+
+
+def test_first_call_in_a_capture():
+    """A process whose first calls are captured into a graph, and replayed."""
+    import subprocess
+    import sys
+    code = """
+import torch
+from kv_cache_quantization_02_b200 import kvq
+torch.manual_seed(0)
+kc, vc = (torch.zeros((9, 2, 16, 128), dtype=torch.int8, device="cuda") for _ in range(2))
+ks, vs = (torch.ones((9, 2), device="cuda") for _ in range(2))
+table = torch.arange(8, dtype=torch.int32, device="cuda").view(1, 8)
+cu = torch.tensor([0, 100], dtype=torch.int32, device="cuda")
+zero, lens = torch.zeros(1, dtype=torch.int32, device="cuda"), torch.full((1,), 100, dtype=torch.int32, device="cuda")
+k, v, q = (torch.randn((100, h, 128), device="cuda").half() for h in (2, 2, 8))
+torch.cuda.synchronize()
+g = torch.cuda.CUDAGraph()
+def run():
+    kvq.paged_write(k, v, cu, zero, table, kc, vc, ks, vs)
+    a, _ = kvq.paged_read(cu, zero, table, kc, vc, ks, vs, n_tokens=100)
+    b = kvq.paged_attention_prefill(q, cu, lens, table, kc, vc, ks, vs, sm_scale=0.1)
+    return a, b, kvq.paged_attention_decode(q[:1], lens, table, kc, vc, ks, vs, sm_scale=0.1)
+with torch.cuda.graph(g):
+    out = run()
+g.replay()
+torch.cuda.synchronize()
+assert all(torch.equal(x, y) for x, y in zip(out, run()))
+assert kvq.kvq_fault_status() == 0
+"""
+    import os
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0, r.stderr[-2000:]
 
 
 def _generate(kvq, c, d, fmt, steps, prompt, Hq, Hkv, D, graph):
