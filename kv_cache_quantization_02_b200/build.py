@@ -1,4 +1,5 @@
-"""Build libkvq.so in-tree with nvcc for sm_100a.
+"""Build libkvq.so in-tree with nvcc for sm_100a, and _kvq_torch.so, the torch
+side of the paged cache's calls, with g++.
 
     python -m kv_cache_quantization_02_b200.build
 
@@ -28,6 +29,8 @@ UNIT_FLAGS = {n: ["--fmad=true"] for n in ("kvq_attn_d64.cu", "kvq_attn_d128.cu"
                                            "kvq_paged_decode.cu", "kvq_paged_prefill.cu")}
 INCLUDE = os.path.join(ROOT, "include")
 LIBRARY = os.path.join(PKG, "libkvq.so")
+TORCH_SOURCE = os.path.join(PKG, "csrc", "kvq_torch.cpp")
+TORCH_MODULE = os.path.join(PKG, "_kvq_torch.so")
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 
 FLAGS = [
@@ -38,6 +41,27 @@ FLAGS = [
     "-shared", "-cudart", "shared",
     "-Xlinker", "-rpath,/usr/local/cuda/lib64",
 ]
+
+
+def build_torch_module() -> str:
+    """Compile the Python module that checks torch tensors and calls the library (host code, linked to it)."""
+    import sysconfig
+
+    import torch
+    from torch.utils import cpp_extension
+
+    includes = [INCLUDE, sysconfig.get_paths()["include"], *cpp_extension.include_paths(),
+                os.path.join(os.path.dirname(os.path.dirname(NVCC)), "include")]
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           *(f"-I{d}" for d in includes), TORCH_SOURCE, "-o", TORCH_MODULE,
+           f"-L{PKG}", "-l:libkvq.so", "-Wl,-rpath,$ORIGIN",
+           *(f"-L{d}" for d in cpp_extension.library_paths()),
+           "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda"]
+    res = subprocess.run(cmd, capture_output=True, text=True)
+    if res.returncode != 0:
+        raise RuntimeError("g++ failed:\n" + res.stdout + res.stderr)
+    return TORCH_MODULE
 
 
 def build(verbose: bool = False, extra: list[str] | None = None) -> str:
@@ -71,6 +95,7 @@ def build(verbose: bool = False, extra: list[str] | None = None) -> str:
         res = subprocess.run(link, capture_output=True, text=True)
         if res.returncode != 0:
             raise RuntimeError("nvcc link failed:\n" + res.stdout + res.stderr)
+    build_torch_module()
     return LIBRARY
 
 

@@ -17,7 +17,7 @@ library is missing, importing this module raises ImportError.
 from __future__ import annotations
 
 import ctypes
-import functools
+import importlib.util
 import os
 
 import torch  # loads libcudart first, so the library shares torch's runtime
@@ -491,97 +491,38 @@ def dequantize(packed: torch.Tensor, scales: torch.Tensor, lam: torch.Tensor,
 
 # ---- the paged 8-bit cache ------------------------------------------------
 #
-# A decode step's calls are short, so these wrappers check each tensor once and
-# call the library directly.
+# Decode steps make these calls for every layer, so the checks of the tensors,
+# the outputs and the call itself are compiled (csrc/kvq_torch.cpp).
 
-_PAGED_FORMAT = {torch.int8: KVQ_INT8, torch.float8_e4m3fn: KVQ_E4M3}
-_PAGED_DTYPE = {torch.float16: KVQ_FP16, torch.bfloat16: KVQ_BF16}
-_F32, _I32, _U8 = torch.float32, torch.int32, torch.uint8
-
-# torch.cuda.current_device() and the handle of current_stream(index) without
-# the objects around them (a microsecond a call)
-_current_device = torch._C._cuda_getDevice
-_current_stream = torch._C._cuda_getCurrentRawStream
-
-
-def _paged_need(t, dtype, shape, index, name):
-    """`t` is a contiguous tensor of this type and shape on CUDA device `index`."""
-    if t.dtype is dtype and t.shape == shape and t.is_contiguous() and t.get_device() == index:
-        return
-    _need(t, dtype, shape, name)
-    raise ValueError(f"{name} must be on cuda:{index} as the other tensors, got {t.device}")
+def _paged_module():
+    path = os.path.join(_PKG, "_kvq_torch.so")
+    if not os.path.exists(path):
+        raise ImportError(f"{path} is not built; run `python -m kv_cache_quantization_02_b200.build`")
+    spec = importlib.util.spec_from_file_location("_kvq_torch", path)
+    module = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(module)
+    return module
 
 
-def _paged_cache(block_table, k_cache, v_cache, k_scales, v_scales):
-    """Checks the cache and its table; (device, format, B, max_blocks, num_blocks, Hkv, block, D)."""
-    if k_cache.dim() != 4 or block_table.dim() != 2:
-        raise ValueError("k_cache must be [num_blocks, Hkv, block, D] and block_table [B, max_blocks]")
-    dtype, shape, index = k_cache.dtype, k_cache.shape, k_cache.get_device()
-    fmt = _PAGED_FORMAT.get(dtype)
-    if fmt is None:
-        raise ValueError(f"k_cache must be torch.int8 or torch.float8_e4m3fn, got {dtype}")
-    if index < 0:
-        raise ValueError("k_cache must be a CUDA tensor")
-    num_blocks, Hkv, block, D = shape
-    B, max_blocks = block_table.shape
-    one = (num_blocks, Hkv)
-    if not (v_cache.dtype is dtype and v_cache.shape == shape and k_scales.dtype is _F32 and k_scales.shape == one
-            and v_scales.dtype is _F32 and v_scales.shape == one and block_table.dtype is _I32
-            and k_cache.is_contiguous() and v_cache.is_contiguous() and k_scales.is_contiguous()
-            and v_scales.is_contiguous() and block_table.is_contiguous()
-            and v_cache.get_device() == k_scales.get_device() == v_scales.get_device()
-            == block_table.get_device() == index):
-        _paged_need(k_cache, dtype, shape, index, "k_cache")
-        _paged_need(v_cache, dtype, shape, index, "v_cache")
-        _paged_need(k_scales, _F32, one, index, "k_scales")
-        _paged_need(v_scales, _F32, one, index, "v_scales")
-        _paged_need(block_table, _I32, (B, max_blocks), index, "block_table")
-    return index, fmt, B, max_blocks, num_blocks, Hkv, block, D
+_paged = _paged_module()
 
 
-def _paged_lists(cu, cu_name, each, each_name, B, index):
-    """Checks offsets [B + 1] and a list [B], int32."""
-    if not (cu.dtype is _I32 and each.dtype is _I32 and cu.shape == (B + 1,) and each.shape == (B,)
-            and cu.is_contiguous() and each.is_contiguous() and cu.get_device() == each.get_device() == index):
-        _paged_need(cu, _I32, (B + 1,), index, cu_name)
-        _paged_need(each, _I32, (B,), index, each_name)
+def _paged_result(result):
+    """What a compiled call returns: a status as an int, or the outputs."""
+    if type(result) is int:
+        if result != KVQ_OK:
+            raise KvqError(result)
+        return None
+    return result
 
 
-def _paged_rows(x, name, D, index):
-    """Checks token rows [n, heads, D] that may lie apart; (element type, n, heads, stride)."""
-    dtype = _PAGED_DTYPE.get(x.dtype)
-    if dtype is None:
-        raise ValueError(f"{name} must be torch.float16 or torch.bfloat16, got {x.dtype}")
-    shape = x.shape
-    if len(shape) != 3 or shape[2] != D:
-        raise ValueError(f"{name} must be [tokens, heads, {D}], got {tuple(shape)}")
-    if x.get_device() != index:
-        raise ValueError(f"{name} must be on cuda:{index} as the cache, got {x.device}")
-    n, heads, _ = shape
-    s0, s1, s2 = x.stride()
-    if s2 != 1 or (s1 != D and heads > 1):
-        raise ValueError(f"{name}: the channels and heads of a token must be contiguous")
-    return dtype, n, heads, s0 if n > 1 else heads * D
-
-
-def _paged_call(index, fn, *args):
-    """fn(*args) with device `index` current; raises KvqError."""
-    if index == _current_device():
-        rc = fn(*args)
-    else:
-        with torch.cuda.device(index):
-            rc = fn(*args)
-    if rc != KVQ_OK:
-        raise KvqError(rc)
-
-
-def _on_stream(fn, stream, index, *args, **kwargs):
+def _on_stream(fn, stream, k_cache, *args):
     """A call under `stream`: what it allocates belongs to that stream, and is
     not handed out again before its work."""
-    if stream.device.index != index:
-        raise ValueError(f"stream is on {stream.device}, the cache on cuda:{index}")
+    if stream.device != k_cache.device:
+        raise ValueError(f"stream is on {stream.device}, the cache on {k_cache.device}")
     with torch.cuda.stream(stream):
-        return fn(*args, **kwargs)
+        return fn(*args)
 
 
 def paged_write(k: torch.Tensor, v: torch.Tensor, cu_tokens: torch.Tensor, start: torch.Tensor,
@@ -595,22 +536,12 @@ def paged_write(k: torch.Tensor, v: torch.Tensor, cu_tokens: torch.Tensor, start
     position p is slot p % block of block block_table[b, p // block] (int32
     [B, max_blocks]).  k_cache, v_cache: int8 or float8_e4m3fn [num_blocks,
     Hkv, block, D] with fp32 scales [num_blocks, Hkv].  This call and the three
-    below run on the current stream of the tensors' device, or on ``stream``."""
+    below run on the current stream of the cache's device, or on ``stream``."""
     if stream is not None:
-        return _on_stream(paged_write, stream, k_cache.get_device(), k, v, cu_tokens, start, block_table, k_cache,
-                          v_cache, k_scales, v_scales)
-    index, fmt, B, max_blocks, num_blocks, Hkv, block, D = _paged_cache(block_table, k_cache, v_cache, k_scales,
-                                                                        v_scales)
-    dtype, n, heads, k_stride = _paged_rows(k, "k", D, index)
-    v_dtype, v_n, v_heads, v_stride = _paged_rows(v, "v", D, index)
-    if heads != Hkv or v_heads != Hkv or v_n != n or v_dtype != dtype:
-        raise ValueError(f"k and v must both be [n, {Hkv}, {D}] of one type, "
-                         f"got {tuple(k.shape)} {k.dtype} and {tuple(v.shape)} {v.dtype}")
-    _paged_lists(cu_tokens, "cu_tokens", start, "start", B, index)
-    _paged_call(index, _lib.kvq_paged_write, k.data_ptr(), v.data_ptr(), dtype, k_stride, v_stride,
-                cu_tokens.data_ptr(), start.data_ptr(), block_table.data_ptr(), B, max_blocks, n, Hkv, D, block, fmt,
-                num_blocks, k_cache.data_ptr(), v_cache.data_ptr(), k_scales.data_ptr(), v_scales.data_ptr(),
-                _current_stream(index))
+        return _on_stream(paged_write, stream, k_cache, k, v, cu_tokens, start, block_table, k_cache, v_cache,
+                          k_scales, v_scales)
+    return _paged_result(_paged.paged_write(k, v, cu_tokens, start, block_table, k_cache, v_cache, k_scales,
+                                            v_scales))
 
 
 def paged_read(cu_tokens: torch.Tensor, start: torch.Tensor, block_table: torch.Tensor, k_cache: torch.Tensor,
@@ -618,50 +549,15 @@ def paged_read(cu_tokens: torch.Tensor, start: torch.Tensor, block_table: torch.
                dtype: torch.dtype = torch.float16, k_out: torch.Tensor | None = None,
                v_out: torch.Tensor | None = None, stream=None):
     """The tokens of paged_write back out of the cache -> (k, v), each
-    [n_tokens, Hkv, D] of `dtype`.  Rows from cu_tokens[B] on are not written."""
+    [n_tokens, Hkv, D] of `dtype`, fp16 or bf16.  Rows from cu_tokens[B] on are
+    not written."""
     if stream is not None:
-        return _on_stream(paged_read, stream, k_cache.get_device(), cu_tokens, start, block_table, k_cache, v_cache,
-                          k_scales, v_scales, n_tokens, dtype, k_out, v_out)
-    index, fmt, B, max_blocks, num_blocks, Hkv, block, D = _paged_cache(block_table, k_cache, v_cache, k_scales,
-                                                                        v_scales)
-    code = _PAGED_DTYPE.get(dtype)
-    if code is None:
+        return _on_stream(paged_read, stream, k_cache, cu_tokens, start, block_table, k_cache, v_cache, k_scales,
+                          v_scales, n_tokens, dtype, k_out, v_out)
+    if dtype is not torch.bfloat16 and dtype is not torch.float16:
         raise ValueError(f"dtype must be torch.float16 or torch.bfloat16, got {dtype}")
-    _paged_lists(cu_tokens, "cu_tokens", start, "start", B, index)
-    shape = (n_tokens, Hkv, D)
-    if k_out is None:
-        k_out = k_cache.new_empty(shape, dtype=dtype)
-    else:
-        _paged_need(k_out, dtype, shape, index, "k_out")
-    if v_out is None:
-        v_out = k_cache.new_empty(shape, dtype=dtype)
-    else:
-        _paged_need(v_out, dtype, shape, index, "v_out")
-    _paged_call(index, _lib.kvq_paged_read, cu_tokens.data_ptr(), start.data_ptr(), block_table.data_ptr(), B,
-                max_blocks, n_tokens, Hkv, D, block, fmt, num_blocks, k_cache.data_ptr(), v_cache.data_ptr(),
-                k_scales.data_ptr(), v_scales.data_ptr(), code, k_out.data_ptr(), v_out.data_ptr(),
-                _current_stream(index))
-    return k_out, v_out
-
-
-@functools.lru_cache(maxsize=4096)
-def _paged_workspace_bytes(size, index, *shape):
-    with torch.cuda.device(index):
-        return size(*shape)
-
-
-def _paged_workspace(workspace, like, size, index, *shape):
-    """(tensor or None, address, bytes): `workspace` True allocates what the library asks for."""
-    if workspace is True:
-        need = _paged_workspace_bytes(size, index, *shape)
-        if need <= 0:
-            return None, 0, 0
-        workspace = like.new_empty(need, dtype=_U8)
-        return workspace, workspace.data_ptr(), need
-    if not isinstance(workspace, torch.Tensor):
-        return None, 0, 0
-    _paged_need(workspace, _U8, (workspace.numel(),), index, "workspace")
-    return workspace, workspace.data_ptr(), workspace.numel()
+    return _paged_result(_paged.paged_read(cu_tokens, start, block_table, k_cache, v_cache, k_scales, v_scales,
+                                           n_tokens, dtype is torch.bfloat16, k_out, v_out))
 
 
 def paged_attention_decode(q: torch.Tensor, seq_len: torch.Tensor, block_table: torch.Tensor, k_cache: torch.Tensor,
@@ -674,26 +570,10 @@ def paged_attention_decode(q: torch.Tensor, seq_len: torch.Tensor, block_table: 
     `window` of them -> [B, Hq, D].  ``workspace``: a uint8 CUDA tensor, True
     to allocate the size the library asks for, or False to run unsplit."""
     if stream is not None:
-        return _on_stream(paged_attention_decode, stream, k_cache.get_device(), q, seq_len, block_table, k_cache,
-                          v_cache, k_scales, v_scales, sm_scale, window, out, workspace)
-    index, fmt, B, max_blocks, num_blocks, Hkv, block, D = _paged_cache(block_table, k_cache, v_cache, k_scales,
-                                                                        v_scales)
-    dtype, n, Hq, q_stride = _paged_rows(q, "q", D, index)
-    if n != B:
-        raise ValueError(f"q must have one row for each of the {B} sequences, got {n}")
-    _paged_need(seq_len, _I32, (B,), index, "seq_len")
-    window = int(window)
-    if out is None:
-        out = q.new_empty((B, Hq, D))
-    else:
-        _paged_need(out, q.dtype, (B, Hq, D), index, "out")
-    ws, ws_ptr, ws_bytes = _paged_workspace(workspace, q, kvq_paged_decode_workspace_bytes, index, B, max_blocks, Hq, Hkv,
-                                            D, block, window)
-    _paged_call(index, _lib.kvq_paged_attention_decode, q.data_ptr(), dtype, q_stride, seq_len.data_ptr(),
-                block_table.data_ptr(), B, max_blocks, Hq, Hkv, D, block, fmt, num_blocks, k_cache.data_ptr(),
-                v_cache.data_ptr(), k_scales.data_ptr(), v_scales.data_ptr(), float(sm_scale), window, out.data_ptr(),
-                ws_ptr, ws_bytes, _current_stream(index))
-    return out
+        return _on_stream(paged_attention_decode, stream, k_cache, q, seq_len, block_table, k_cache, v_cache,
+                          k_scales, v_scales, sm_scale, window, out, workspace)
+    return _paged_result(_paged.paged_attention_decode(q, seq_len, block_table, k_cache, v_cache, k_scales, v_scales,
+                                                       sm_scale, window, out, workspace))
 
 
 def paged_attention_prefill(q: torch.Tensor, cu_q: torch.Tensor, seq_len: torch.Tensor, block_table: torch.Tensor,
@@ -707,21 +587,7 @@ def paged_attention_prefill(q: torch.Tensor, cu_q: torch.Tensor, seq_len: torch.
     paged_attention_decode -> [n, Hq, D].  Rows from cu_q[B] on are not
     written."""
     if stream is not None:
-        return _on_stream(paged_attention_prefill, stream, k_cache.get_device(), q, cu_q, seq_len, block_table,
-                          k_cache, v_cache, k_scales, v_scales, sm_scale, window, out, workspace)
-    index, fmt, B, max_blocks, num_blocks, Hkv, block, D = _paged_cache(block_table, k_cache, v_cache, k_scales,
-                                                                        v_scales)
-    dtype, n, Hq, q_stride = _paged_rows(q, "q", D, index)
-    _paged_lists(cu_q, "cu_q", seq_len, "seq_len", B, index)
-    window = int(window)
-    if out is None:
-        out = q.new_empty((n, Hq, D))
-    else:
-        _paged_need(out, q.dtype, (n, Hq, D), index, "out")
-    ws, ws_ptr, ws_bytes = _paged_workspace(workspace, q, kvq_paged_prefill_workspace_bytes, index, B, max_blocks, n, Hq,
-                                            Hkv, D, block, window)
-    _paged_call(index, _lib.kvq_paged_attention_prefill, q.data_ptr(), dtype, q_stride, cu_q.data_ptr(),
-                seq_len.data_ptr(), block_table.data_ptr(), B, max_blocks, n, Hq, Hkv, D, block, fmt, num_blocks,
-                k_cache.data_ptr(), v_cache.data_ptr(), k_scales.data_ptr(), v_scales.data_ptr(), float(sm_scale), window,
-                out.data_ptr(), ws_ptr, ws_bytes, _current_stream(index))
-    return out
+        return _on_stream(paged_attention_prefill, stream, k_cache, q, cu_q, seq_len, block_table, k_cache, v_cache,
+                          k_scales, v_scales, sm_scale, window, out, workspace)
+    return _paged_result(_paged.paged_attention_prefill(q, cu_q, seq_len, block_table, k_cache, v_cache, k_scales,
+                                                        v_scales, sm_scale, window, out, workspace))

@@ -630,5 +630,65 @@ def test_empty_calls(kvq):
     assert kvq.paged_attention_prefill(none, d.cu, d.start, d.table, *d.cache(), sm_scale=1.0).shape == (0, 2, 128)
 
 
+def test_wrong_tensors(kvq):
+    """Each wrong argument is refused by name; small workspaces are not used, and statuses become KvqError."""
+    c = Case(128, 2, 16, "int8", [3, 40], [5, 6], seed=25, R=2)
+    d = c.cuda()
+    k, q = c.rows(2, "fp16").cuda(), c.rows(4, "fp16").cuda()
+    before = [x.clone() for x in d.cache()]
+    cache = list(d.cache())
+
+    def swapped(i, x):
+        return [x if j == i else y for j, y in enumerate(cache)]
+
+    bad_caches = [
+        ("k_cache", swapped(0, d.kc.view(torch.uint8))), ("k_cache", swapped(0, d.kc[0])),
+        ("v_cache", swapped(1, d.vc[1:])), ("v_cache", swapped(1, d.vc.view(torch.float8_e4m3fn))),
+        ("v_cache", swapped(1, d.vc.transpose(1, 2).contiguous().transpose(1, 2))), ("v_cache", swapped(1, d.vc.cpu())),
+        ("k_scales", swapped(2, d.ks.double())), ("v_scales", swapped(3, d.vs[:, :1])), ("k_scales", swapped(2, d.ks.cpu())),
+    ]
+    for name, bad in bad_caches:
+        for call in (lambda: kvq.paged_write(k, k, d.cu, d.start, d.table, *bad),
+                     lambda: kvq.paged_read(d.cu, d.start, d.table, *bad, n_tokens=11),
+                     lambda: kvq.paged_attention_decode(q[:2], d.seq_len, d.table, *bad, sm_scale=1.0),
+                     lambda: kvq.paged_attention_prefill(q, d.cu, d.seq_len, d.table, *bad, sm_scale=1.0)):
+            with pytest.raises(ValueError, match=name):
+                call()
+    for name, args in (("cu_tokens", (k, k, d.cu.long(), d.start, d.table)), ("cu_tokens", (k, k, d.cu[1:], d.start, d.table)),
+                       ("start", (k, k, d.cu, d.start.cpu(), d.table)), ("block_table", (k, k, d.cu, d.start, d.table.long())),
+                       ("block_table", (k, k, d.cu, d.start, d.table[0])), ("k and v", (k, k[1:], d.cu, d.start, d.table)),
+                       ("k and v", (k, k.bfloat16(), d.cu, d.start, d.table)), ("k and v", (q, q, d.cu, d.start, d.table)),
+                       ("k must", (k.float(), k, d.cu, d.start, d.table)), ("v must", (k, k[:, :, :64], d.cu, d.start, d.table)),
+                       ("k: the channels", (k.transpose(0, 1).contiguous().transpose(0, 1), k, d.cu, d.start, d.table)),
+                       ("k must", (k.cpu(), k, d.cu, d.start, d.table))):
+        with pytest.raises(ValueError, match=name):
+            kvq.paged_write(*args, *cache)
+    for name, kw in (("out", dict(out=q[:2].float())), ("out", dict(out=q[:3])), ("out", dict(out=q[:2].cpu())),
+                     ("workspace", dict(workspace=torch.empty(9, device="cuda")))):
+        with pytest.raises(ValueError, match=name):
+            kvq.paged_attention_decode(q[:2], d.seq_len, d.table, *cache, sm_scale=1.0, **kw)
+    with pytest.raises(ValueError, match="q must have one row"):
+        kvq.paged_attention_decode(q, d.seq_len, d.table, *cache, sm_scale=1.0)
+    with pytest.raises(ValueError, match="torch.Tensor"):
+        kvq.paged_attention_decode(None, d.seq_len, d.table, *cache, sm_scale=1.0)
+    with pytest.raises(ValueError, match="dtype"):
+        kvq.paged_read(d.cu, d.start, d.table, *cache, n_tokens=11, dtype=torch.float32)
+    with pytest.raises(ValueError, match="n_tokens"):
+        kvq.paged_read(d.cu, d.start, d.table, *cache, n_tokens=-1)
+    with pytest.raises(TypeError):
+        kvq.paged_attention_decode(q[:2], d.seq_len, d.table, *cache, sm_scale="1")
+    for kw, status in ((dict(window=-1), -5), (dict(sm_scale=math.nan), -5)):
+        with pytest.raises(kvq.KvqError) as e:
+            kvq.paged_attention_decode(q[:2], d.seq_len, d.table, *cache, **dict(dict(sm_scale=1.0), **kw))
+        assert e.value.status == status
+    with pytest.raises(kvq.KvqError) as e:
+        kvq.paged_read(d.cu, d.start, d.table, *(x[:, :, :8].contiguous() for x in cache[:2]), *cache[2:], n_tokens=11)
+    assert e.value.status == -7                                   # blocks of 8 tokens
+    want = kvq.paged_attention_decode(q[:2], d.seq_len, d.table, *cache, sm_scale=1.0, workspace=False)
+    small = torch.empty(64, dtype=torch.uint8, device="cuda")
+    assert same(kvq.paged_attention_decode(q[:2], d.seq_len, d.table, *cache, sm_scale=1.0, workspace=small), want)
+    assert all(same(x, y) for x, y in zip(before, d.cache()))
+
+
 def test_formats_are_named(kvq):
     assert set(FORMATS.values()) == set(QMAX)
