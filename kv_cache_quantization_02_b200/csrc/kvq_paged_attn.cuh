@@ -23,7 +23,9 @@ namespace kvqp {
 constexpr float kBoost = 6.0f, kLazy = 8.0f;
 
 // Thread blocks of the decode kernel that an SM holds (registers and shared
-// memory); a split call launches that many for each SM.
+// memory); a split call launches that many for each SM.  Measured on 64 ragged
+// sequences of up to 4K tokens: D = 64 38 us with four, 44 with five, 41 with
+// three; D = 256 69 us with three (168 registers), 75 with two.
 template <int D>
 constexpr int kDecodeBlocks = D == 64 ? 4 : 3;
 

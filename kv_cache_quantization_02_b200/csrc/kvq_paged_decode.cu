@@ -18,6 +18,12 @@
 // item boundaries, so the ring stays full.  Copies rather than tensor maps:
 // a tile of 16-token blocks is two pieces, and a call needs no map.
 //
+// Measured at D = 128, 32 query heads on 8: 16 sequences of 32K tokens 169 us
+// (6.35 TB/s) with two half-tiles a warp, 177 us with three, 184 us with four:
+// 12 warps an SM ask for enough, more only queues.  64 ragged sequences of up
+// to 4K 62 us (5.1 TB/s), of which about 8 us are start and join; 16 warps an
+// SM (128 registers) took 70 us.
+//
 // Both products run as m16n8k16 MMAs on fp16 with fp32 sums, codes as A:
 //   scores   M = 16 keys, K = 16 channels, N = 8 heads.  A lane's word of four
 //            codes gives the fragments of one k-step by the channel order
@@ -47,7 +53,7 @@ constexpr int kMetaSlots = 8;                     // tiles whose scales are kept
 template <int D>
 struct Decode {
   static constexpr int HALF = kTile * D;          // bytes of one half-tile: 32 keys of K, or of V
-  static constexpr int NST = D == 64 ? 4 : 2;
+  static constexpr int NST = D == 64 ? 4 : 2;     // half-tiles in flight a warp (see above)
   static constexpr int RING = kWarps * NST * HALF;
   static constexpr int XP = D == 256 ? 2 : 1;     // parts in which a block joins its warps' sums
   static constexpr int XCH = 2 * kHeads * D * 4 / XP;       // two warps' sums of a part
