@@ -74,8 +74,8 @@ struct Prefill {
   static constexpr int TILE = KT * D * 2;         // fp16 bytes of a K or V tile
   static constexpr int STAGES = 2;
   static constexpr int META = 4 * NSUB * 16;      // scales of four tiles
-  static constexpr int NBAR = 4 * STAGES + 4 + 3 * 4;
-  static constexpr int SMEM = 1024 + QBYTES + 2 * STAGES * TILE + META + ROWS * 4 + NBAR * 8 + 64;
+  static constexpr int NBAR = 4 * STAGES + 4 + 3 * 4 + 1;
+  static constexpr int SMEM = 1024 + QBYTES + 2 * STAGES * TILE + META + ROWS * 4 + 128 * 8 + NBAR * 8 + 64;
   // tensor memory columns: two score buffers (the weights over them) for each
   // 128 rows, then the outputs
   static constexpr int O0 = MT * 2 * kStep;
@@ -284,9 +284,11 @@ __global__ void __launch_bounds__(kThreads, 1) paged_prefill_kernel(AttnArgs a, 
   uint8_t* vbuf = kbuf + ST * C::TILE;
   float4* meta = reinterpret_cast<float4*>(vbuf + ST * C::TILE);               // [4][NSUB]: S_K, log2 S_V, 1 / S_V
   float* unit = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(meta) + C::META);
-  uint64_t* bars = reinterpret_cast<uint64_t*>(unit + C::ROWS);
+  float2* second = reinterpret_cast<float2*>(unit + C::ROWS);                  // [128]: the second set's references, sums
+  uint64_t* bars = reinterpret_cast<uint64_t*>(second + 128);
   uint64_t *k_full = bars, *k_empty = bars + ST, *v_full = bars + 2 * ST, *v_empty = bars + 3 * ST;
   uint64_t *meta_full = bars + 4 * ST, *s_full = meta_full + 4, *p_full = s_full + 4, *o_full = p_full + 4;
+  uint64_t* joined = o_full + 4;
   uint32_t* shared_word = reinterpret_cast<uint32_t*>(bars + C::NBAR);         // the tensor memory's address
 
   const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(kAll, tid >> 5, 0);
@@ -302,7 +304,17 @@ __global__ void __launch_bounds__(kThreads, 1) paged_prefill_kernel(AttnArgs a, 
                  :: "r"(smem_addr(shared_word)), "n"(C::COLS) : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
-  const int sets = C::MT == 2 && j.count > 128 ? 2 : 1;     // of 128 rows: an empty second one is left out
+  // Up to 128 rows: the second set of softmax warps takes the odd key tiles of
+  // the same rows, and the two sets' sums are joined in the end.  (Stage 1 of the
+  // tiles in shared memory is then the second set's alone.)
+  const int sets = C::MT == 2 && j.count > 128 ? 2 : 1;
+  const bool dual = C::MT == 2 && sets == 1;
+  // a set's steps: how many, and the tile of the i-th
+  auto steps_of = [&](int mt) {
+    if (!dual) return j.steps;
+    return j.tiles > mt ? (j.tiles - mt + 1) / 2 * 2 - (((j.tiles - 1) & 1) == mt ? j.steps & 1 : 0) : 0;
+  };
+  auto tile_of = [&](int i, int mt) { return C::STEPS == 1 ? i : dual ? mt + (i & ~1) : i >> 1; };
   if (tid == 0) {
     for (int i = 0; i < ST; ++i) {
       mbar_init(&k_full[i], 4); mbar_init(&v_full[i], 4);
@@ -312,6 +324,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_prefill_kernel(AttnArgs a, 
     // per 128 rows, steps alternate between two of each: a wait is then never two
     // phases behind, which a parity could not tell from none
     for (int i = 0; i < 4; ++i) { mbar_init(&s_full[i], 1); mbar_init(&p_full[i], 4); mbar_init(&o_full[i], 1); }
+    mbar_init(joined, 4);
     mbar_fence_init();
   }
 
@@ -374,15 +387,18 @@ __global__ void __launch_bounds__(kThreads, 1) paged_prefill_kernel(AttnArgs a, 
   if (warp < 8) {
     // ---- softmax
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" :: "n"(kSoftmaxRegs));
-    const int mt = warp >> 2;
-    if (mt < sets) {
-      const int r = mt * 128 + (warp & 3) * 32 + lane;
+    const int mt = warp >> 2, own = (warp & 3) * 32 + lane;
+    if (mt < C::MT) {
+      const int r = (dual ? 0 : mt * 128) + own, steps = steps_of(mt);
       const uint32_t lanes = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
       const uint32_t o_at = lanes + C::O0 + mt * D;
       const bool live = r < j.count;
       const int row = j.row0 + r;
-      const int pos = live ? j.L - j.n + row / a.R : -1;    // this row sees keys .. pos
-      const int low = a.window > 0 ? pos - a.window + 1 : 0;
+      // this row sees the keys low .. pos (a row that is not there: all of them, and
+      // its weights are nobody's)
+      const int pos = live ? j.L - j.n + row / a.R : INT32_MAX;
+      const int low = a.window > 0 && live ? pos - a.window + 1 : 0;
+      const bool rest = !__any_sync(kAll, live);            // no row of this warp is there
       const float u = unit[r];
       // over the warp: tiles inside [wlow, wpos] need no mask
       int wpos = pos, wlow = low;
@@ -393,13 +409,17 @@ __global__ void __launch_bounds__(kThreads, 1) paged_prefill_kernel(AttnArgs a, 
       }
       float M = -INFINITY, l = 0.0f;
 #pragma unroll 1
-      for (int i = 0; i < j.steps; ++i) {
-        const int buf = mt * 2 + (i & 1), tile = i / C::STEPS;
+      for (int i = 0; i < steps; ++i) {
+        const int buf = mt * 2 + (i & 1), tile = tile_of(i, mt);
         const uint32_t s_at = lanes + buf * kStep;
         if (!wait(&s_full[buf], (i >> 1) & 1) || !wait(&meta_full[tile & 3], (tile >> 2) & 1)) break;
         tmem_fence_after();
+        if (rest) {
+          if (lane == 0) mbar_arrive(&p_full[buf]);
+          continue;
+        }
         const float4* sc = meta + (tile & 3) * NSUB + (C::STEPS == 2 ? (i & 1) * 4 : 0);
-        const int key0 = j.first + i * kStep;
+        const int key0 = j.first + tile * KT + (C::STEPS == 2 ? (i & 1) * kStep : 0);
         auto step = [&](auto edge) -> bool {
           uint32_t s[2][32], w[kStep / 2];
           tmem_ld32(s[0], s_at);
@@ -470,21 +490,57 @@ __global__ void __launch_bounds__(kThreads, 1) paged_prefill_kernel(AttnArgs a, 
         if (lane == 0) mbar_arrive(&p_full[buf]);
       }
       // ---- outputs
-      if (j.steps > 0 && wait(&o_full[mt * 2 + ((j.steps - 1) & 1)], ((j.steps - 1) >> 1) & 1)) tmem_fence_after();
-      const bool some = j.steps > 0 && ok;
+      if (steps > 0 && wait(&o_full[mt * 2 + ((steps - 1) & 1)], ((steps - 1) >> 1) & 1)) tmem_fence_after();
+      const bool some = steps > 0 && ok;
+      // The second set leaves its sums in stage 1 of K and V, column by column.
+      auto spare = [&](int c) {
+        return reinterpret_cast<float*>((c < D / 2 ? kbuf : vbuf) + C::TILE) + (c % (D / 2)) * 128 + own;
+      };
+      const bool joins = dual && mt == 0 && steps_of(1) > 0;
+      float f0 = 1.0f, f1 = 0.0f;
+      if (dual && mt == 1 && some) {
+#pragma unroll 1
+        for (int c = 0; c < D; c += 32) {
+          uint32_t o[32];
+          tmem_ld32(o, o_at + c);
+          tmem_wait_ld();
+#pragma unroll
+          for (int e = 0; e < 32; ++e) spare(c)[e * 128] = __uint_as_float(o[e]);
+        }
+        second[own] = make_float2(M, l);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(joined);
+      }
+      if (joins && wait(joined, 0)) {
+        const float2 x = second[own];
+        const float now = fmaxf(M, x.x), ref = now == -INFINITY ? 0.0f : now;
+        f0 = exp2_approx(M - ref);
+        f1 = exp2_approx(x.x - ref);
+        l = l * f0 + x.y * f1;
+        M = now;
+      }
+      auto outputs = [&](uint32_t (&o)[32], int c) {        // 32 columns of O
+        if (some) {
+          tmem_ld32(o, o_at + c);
+          tmem_wait_ld();
+        } else {
+#pragma unroll
+          for (int e = 0; e < 32; ++e) o[e] = 0;
+        }
+        if (joins) {
+#pragma unroll
+          for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f0 + spare(c)[e * 128] * f1);
+        }
+      };
       const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-      if (ok && nsplit > 1) {
+      if (dual && mt == 1) {
+        // the first set writes
+      } else if (ok && nsplit > 1) {
         float* part = a.part + ((j.tile * nsplit + j.split) * C::ROWS + r) * (D + 4);
 #pragma unroll 1
         for (int c = 0; c < D / 32; ++c) {
           uint32_t o[32];
-          if (some) {
-            tmem_ld32(o, o_at + 32 * c);
-            tmem_wait_ld();
-          } else {
-#pragma unroll
-            for (int e = 0; e < 32; ++e) o[e] = 0;
-          }
+          outputs(o, 32 * c);
           if (live) {                                       // columns hold channels 0, 2, 1, 3 of each four
 #pragma unroll
             for (int e = 0; e < 32; e += 4)
@@ -499,13 +555,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_prefill_kernel(AttnArgs a, 
 #pragma unroll 1
         for (int c = 0; c < D / 32; ++c) {
           uint32_t o[32];
-          if (some) {
-            tmem_ld32(o, o_at + 32 * c);
-            tmem_wait_ld();
-          } else {
-#pragma unroll
-            for (int e = 0; e < 32; ++e) o[e] = 0;
-          }
+          outputs(o, 32 * c);
 #pragma unroll
           for (int e = 0; e < 32; e += 8) {
             uint32_t h[4];
@@ -539,25 +589,26 @@ __global__ void __launch_bounds__(kThreads, 1) paged_prefill_kernel(AttnArgs a, 
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" :: "n"(kIssuerRegs));
     {
       // ---- the MMAs
-      if (warp < kIssuer + sets && j.tiles > 0) {
+      if (warp < kIssuer + C::MT && j.tiles > 0) {
         const int mt = warp - kIssuer;
         constexpr uint32_t sdesc = kMmaDesc<kStep, false>, odesc = kMmaDesc<D, true>;
         const uint32_t one = elect_one();
         const uint64_t qd = matrix_desc(smem_addr(qs), 16, 1024), kd = matrix_desc(smem_addr(kbuf), 16, 1024);
         const uint64_t vd = matrix_desc(smem_addr(vbuf), KT * 128, 1024);
         // (start addresses count in 16 bytes)
+        const int qset = dual ? 0 : mt;
         auto scores = [&](int i) {                  // step i's, into its buffer
-          const int tile = i / C::STEPS;
+          const int tile = tile_of(i, mt);
           const uint64_t kt = kd + (tile % ST) * (C::TILE / 16) + (C::STEPS == 2 ? (i & 1) * (kStep * 128 / 16) : 0);
 #pragma unroll
           for (int k = 0; k < D / 16; ++k)
-            mma_ss(one, tmem + (mt * 2 + (i & 1)) * kStep, qd + (mt * C::CB + k / 4) * (16384 / 16) + (k % 4) * 2,
+            mma_ss(one, tmem + (mt * 2 + (i & 1)) * kStep, qd + (qset * C::CB + k / 4) * (16384 / 16) + (k % 4) * 2,
                    kt + (k / 4) * (KT * 128 / 16) + (k % 4) * 2, sdesc, k > 0);
           mma_commit(one, &s_full[mt * 2 + (i & 1)]);
           if ((i + 1) % C::STEPS == 0) mma_commit(one, &k_empty[tile % ST]);
         };
         auto values = [&](int i) {
-          const int tile = i / C::STEPS;
+          const int tile = tile_of(i, mt);
           const uint64_t vt = vd + (tile % ST) * (C::TILE / 16) + (C::STEPS == 2 ? (i & 1) * (kStep * 128 / 16) : 0);
 #pragma unroll
           for (int k = 0; k < kStep / 16; ++k)
@@ -568,12 +619,12 @@ __global__ void __launch_bounds__(kThreads, 1) paged_prefill_kernel(AttnArgs a, 
         };
         // K and V tiles are waited for at their first steps
         auto keys_in = [&](int i) {
-          const int tile = i / C::STEPS;
+          const int tile = tile_of(i, mt);
           if (i % C::STEPS == 0) wait(&k_full[tile % ST], (tile / ST) & 1);
           tmem_fence_after();
           return ok;
         };
-        const int n = __shfl_sync(kAll, j.steps, 0);
+        const int n = __shfl_sync(kAll, steps_of(mt), 0);
 #pragma unroll 1
         for (int i = 0; i < 2 && i < n; ++i) {
           if (!keys_in(i)) break;
@@ -581,7 +632,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_prefill_kernel(AttnArgs a, 
         }
 #pragma unroll 1
         for (int i = 0; i < n && ok; ++i) {
-          const int tile = i / C::STEPS;
+          const int tile = tile_of(i, mt);
           if (i % C::STEPS == 0 && !wait(&v_full[tile % ST], (tile / ST) & 1)) break;
           if (!wait(&p_full[mt * 2 + (i & 1)], (i >> 1) & 1)) break;
           tmem_fence_after();
