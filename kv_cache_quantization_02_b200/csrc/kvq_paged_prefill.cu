@@ -328,6 +328,17 @@ __global__ void __launch_bounds__(kThreads, 1) paged_prefill_kernel(AttnArgs a, 
     mbar_fence_init();
   }
 
+  // The converters' first tile: its loads go out before the queries'.
+  const bool is_v = warp >= kFirstV;
+  const uint8_t* codes = is_v ? a.c.vc : a.c.kc;
+  const int which = warp & 3;
+  Share<D> next;
+  int rows = -1;                                  // the parts of the tile in `next`
+  if (warp >= kFirstK && warp < kIssuer && j.tiles > 0) {
+    rows = part_row<D>(a, j, j.first, lane, bad);
+    next.template load<FMT>(codes, rows, j.L - j.first, which, lane);
+  }
+
   // ---- the query rows, fp16 with a power of two each, channels in code order:
   // a lane has 8 channels, a row D / 8 lanes, and all loads of a warp are in
   // flight before the first is used
@@ -651,18 +662,10 @@ __global__ void __launch_bounds__(kThreads, 1) paged_prefill_kernel(AttnArgs a, 
     {
       // ---- codes to fp16, the next tile's loads in flight over this one's
       // conversion and wait
-      const bool is_v = warp >= kFirstV;
-      const uint8_t* codes = is_v ? a.c.vc : a.c.kc;
       uint64_t *full = is_v ? v_full : k_full, *empty = is_v ? v_empty : k_empty;
       const uint32_t base = smem_addr(is_v ? vbuf : kbuf);
-      const int which = (warp - kFirstK) & 3;
-      Share<D> next;
-      int rows = -1, rows2 = -1;                  // the parts of the tile in `next`, and of the one after it
-      if (j.tiles > 0) {
-        rows = part_row<D>(a, j, j.first, lane, bad);
-        next.template load<FMT>(codes, rows, j.L - j.first, which, lane);
-        if (j.tiles > 1) rows2 = part_row<D>(a, j, j.first + KT, lane, bad);
-      }
+      int rows2 = -1;                             // the parts of the tile after the one in `next`
+      if (j.tiles > 1) rows2 = part_row<D>(a, j, j.first + KT, lane, bad);
 #pragma unroll 1
       for (int i = 0; i < j.tiles; ++i) {
         const int st = i % ST;
