@@ -423,7 +423,8 @@ __global__ void __launch_bounds__(kThreads, 1) paged_prefill_kernel(AttnArgs a, 
       for (int i = 0; i < steps; ++i) {
         const int buf = mt * 2 + (i & 1), tile = tile_of(i, mt);
         const uint32_t s_at = lanes + buf * kStep;
-        if (!wait(&s_full[buf], (i >> 1) & 1) || !wait(&meta_full[tile & 3], (tile >> 2) & 1)) break;
+        // (the scales come first)
+        if (!wait(&meta_full[tile & 3], (tile >> 2) & 1) || !wait(&s_full[buf], (i >> 1) & 1)) break;
         tmem_fence_after();
         if (rest) {
           if (lane == 0) mbar_arrive(&p_full[buf]);
@@ -645,15 +646,13 @@ __global__ void __launch_bounds__(kThreads, 1) paged_prefill_kernel(AttnArgs a, 
         for (int i = 0; i < n && ok; ++i) {
           const int tile = tile_of(i, mt);
           if (i % C::STEPS == 0 && !wait(&v_full[tile % ST], (tile / ST) & 1)) break;
+          if (i + 2 < n && !keys_in(i + 2)) break;          // there before the weights are
           if (!wait(&p_full[mt * 2 + (i & 1)], (i >> 1) & 1)) break;
           tmem_fence_after();
           values(i);
           // the buffer is free once that product has read it, which is before
           // the next one of this thread writes it
-          if (i + 2 < n) {
-            if (!keys_in(i + 2)) break;
-            scores(i + 2);
-          }
+          if (i + 2 < n) scores(i + 2);
         }
       }
     }
