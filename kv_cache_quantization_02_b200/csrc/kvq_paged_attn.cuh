@@ -99,6 +99,6 @@ __device__ __forceinline__ int sequence_length(const AttnArgs& a, int b, unsigne
 __attribute__((visibility("hidden"))) int kvq_paged_decode_launch(const kvqp::AttnArgs& a, int format, int grid,
                                                                   cudaStream_t st, cudaError_t& err);
 __attribute__((visibility("hidden"))) unsigned int kvq_paged_decode_fault_word(int clear);
-__attribute__((visibility("hidden"))) int kvq_paged_prefill_launch(const kvqp::AttnArgs& a, int format, int nsplit,
-                                                                   cudaStream_t st, cudaError_t& err);
+__attribute__((visibility("hidden"))) int kvq_paged_prefill_launch(const kvqp::AttnArgs& a, int format, int64_t whole,
+                                                                   int nsplit, cudaStream_t st, cudaError_t& err);
 __attribute__((visibility("hidden"))) unsigned int kvq_paged_prefill_fault_word(int clear);

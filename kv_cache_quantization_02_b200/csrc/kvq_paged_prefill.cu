@@ -73,6 +73,7 @@ struct Prefill {
   static constexpr int QBYTES = ROWS * D * 2;
   static constexpr int TILE = KT * D * 2;         // fp16 bytes of a K or V tile
   static constexpr int STAGES = 2;
+  static constexpr int PART = ROWS * (D + 2);     // floats of a tile's partial sums, references and sums of weights
   static constexpr int META = 4 * NSUB * 16;      // scales of four tiles
   static constexpr int NBAR = 4 * STAGES + 4 + 3 * 4 + 1;
   static constexpr int SMEM = 1024 + QBYTES + 2 * STAGES * TILE + META + ROWS * 4 + 128 * 8 + NBAR * 8 + 64;
@@ -176,17 +177,24 @@ struct Job {
   int row0, count, q0;        // q0: the sequence's first row in the packed queries
   int lo, hi;                 // keys that some row sees
   int first, tiles, steps;    // first key of the first tile; tiles and steps of this split
-  int split;
-  int64_t tile;               // the tile's number, for partial sums
+  int split, nsplit;
+  int64_t tile;               // of a split tile: its number among them, for partial sums
 };
 
 template <int D>
-__device__ __forceinline__ bool find_job(const AttnArgs& a, int nsplit, Job& j, unsigned& bad) {
+__device__ __forceinline__ bool find_job(const AttnArgs& a, int whole, int nsplit, Job& j, unsigned& bad) {
   using C = Prefill<D>;
   unsigned x = blockIdx.x;
-  j.split = static_cast<int>(x % static_cast<unsigned>(nsplit));
-  x /= static_cast<unsigned>(nsplit);
-  j.tile = x;
+  j.split = 0;
+  j.nsplit = 1;
+  if (x >= static_cast<unsigned>(whole)) {
+    x -= static_cast<unsigned>(whole);
+    j.nsplit = nsplit;
+    j.split = static_cast<int>(x % static_cast<unsigned>(nsplit));
+    x /= static_cast<unsigned>(nsplit);
+    j.tile = x;
+    x += static_cast<unsigned>(whole);
+  }
   j.kvh = static_cast<int>(x % static_cast<unsigned>(a.c.Hkv));
   // the last tiles of a sequence see most keys: they start first
   const int64_t items = (a.total_q * a.R >> C::LOG_ROWS) + a.c.B;
@@ -211,8 +219,8 @@ __device__ __forceinline__ bool find_job(const AttnArgs& a, int nsplit, Job& j, 
   j.first = j.lo / C::KT * C::KT;
   const int tiles = j.hi > j.lo ? (j.hi - j.first + C::KT - 1) / C::KT : 0;
   // (tiles < 2^25 and nsplit <= 16)
-  const int t0 = static_cast<int>(static_cast<unsigned>(tiles * j.split) / static_cast<unsigned>(nsplit));
-  const int t1 = static_cast<int>(static_cast<unsigned>(tiles * (j.split + 1)) / static_cast<unsigned>(nsplit));
+  const int t0 = static_cast<int>(static_cast<unsigned>(tiles * j.split) / static_cast<unsigned>(j.nsplit));
+  const int t1 = static_cast<int>(static_cast<unsigned>(tiles * (j.split + 1)) / static_cast<unsigned>(j.nsplit));
   j.first += t0 * C::KT;
   j.tiles = t1 - t0;
   j.steps = j.tiles > 0 ? min(j.tiles * C::STEPS, (j.hi - j.first + kStep - 1) / kStep) : 0;
@@ -274,7 +282,7 @@ struct Share {
 };
 
 template <int D, int FMT>
-__global__ void __launch_bounds__(kThreads, 1) paged_prefill_kernel(AttnArgs a, int nsplit) {
+__global__ void __launch_bounds__(kThreads, 1) paged_prefill_kernel(AttnArgs a, int whole, int nsplit) {
   using C = Prefill<D>;
   constexpr int KT = C::KT, NSUB = C::NSUB, ST = C::STAGES;
   extern __shared__ uint8_t raw_sm[];
@@ -294,7 +302,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_prefill_kernel(AttnArgs a, 
   const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(kAll, tid >> 5, 0);
   unsigned bad = 0;
   Job j;
-  if (!find_job<D>(a, nsplit, j, bad)) {
+  if (!find_job<D>(a, whole, nsplit, j, bad)) {
     if (bad && tid == 0) atomicOr(&g_prefill_fault, bad);
     return;
   }
@@ -547,8 +555,9 @@ __global__ void __launch_bounds__(kThreads, 1) paged_prefill_kernel(AttnArgs a, 
       const float inv = l == 0.0f ? 0.0f : 1.0f / l;
       if (dual && mt == 1) {
         // the first set writes
-      } else if (ok && nsplit > 1) {
-        float* part = a.part + ((j.tile * nsplit + j.split) * C::ROWS + r) * (D + 4);
+      } else if (ok && j.nsplit > 1) {
+        // unit by unit (four channels), all rows of a unit next to one another
+        float* part = a.part + (j.tile * j.nsplit + j.split) * C::PART;
 #pragma unroll 1
         for (int c = 0; c < D / 32; ++c) {
           uint32_t o[32];
@@ -556,10 +565,11 @@ __global__ void __launch_bounds__(kThreads, 1) paged_prefill_kernel(AttnArgs a, 
           if (live) {                                       // columns hold channels 0, 2, 1, 3 of each four
 #pragma unroll
             for (int e = 0; e < 32; e += 4)
-              *reinterpret_cast<uint4*>(part + 32 * c + e) = make_uint4(o[e], o[e + 2], o[e + 1], o[e + 3]);
+              *reinterpret_cast<uint4*>(part + ((8 * c + e / 4) * C::ROWS + r) * 4) =
+                  make_uint4(o[e], o[e + 2], o[e + 1], o[e + 3]);
           }
         }
-        if (live) *reinterpret_cast<float2*>(part + D) = make_float2(M, l);
+        if (live) *reinterpret_cast<float2*>(part + D * C::ROWS + 2 * r) = make_float2(M, l);
       } else if (ok) {
         // through shared memory, where the queries are no longer needed, so that
         // rows go out whole: this warp's 32 rows, 16-byte unit c at c ^ (row mod 8)
@@ -607,7 +617,8 @@ __global__ void __launch_bounds__(kThreads, 1) paged_prefill_kernel(AttnArgs a, 
         const uint32_t one = elect_one();
         const uint64_t qd = matrix_desc(smem_addr(qs), 16, 1024), kd = matrix_desc(smem_addr(kbuf), 16, 1024);
         const uint64_t vd = matrix_desc(smem_addr(vbuf), KT * 128, 1024);
-        // (start addresses count in 16 bytes)
+        // (start addresses count in 16 bytes.  A tile's place is handed back only
+        // where a later tile takes it: no arrival is left for after the block's end.)
         const int qset = dual ? 0 : mt;
         auto scores = [&](int i) {                  // step i's, into its buffer
           const int tile = tile_of(i, mt);
@@ -617,7 +628,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_prefill_kernel(AttnArgs a, 
             mma_ss(one, tmem + (mt * 2 + (i & 1)) * kStep, qd + (qset * C::CB + k / 4) * (16384 / 16) + (k % 4) * 2,
                    kt + (k / 4) * (KT * 128 / 16) + (k % 4) * 2, sdesc, k > 0);
           mma_commit(one, &s_full[mt * 2 + (i & 1)]);
-          if ((i + 1) % C::STEPS == 0) mma_commit(one, &k_empty[tile % ST]);
+          if ((i + 1) % C::STEPS == 0 && tile + ST < j.tiles) mma_commit(one, &k_empty[tile % ST]);
         };
         auto values = [&](int i) {
           const int tile = tile_of(i, mt);
@@ -627,7 +638,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_prefill_kernel(AttnArgs a, 
             mma_ts(one, tmem + C::O0 + mt * D, tmem + (mt * 2 + (i & 1)) * kStep + 8 * k, vt + k * (2048 / 16), odesc,
                    i > 0 || k > 0);
           mma_commit(one, &o_full[mt * 2 + (i & 1)]);
-          if ((i + 1) % C::STEPS == 0) mma_commit(one, &v_empty[tile % ST]);
+          if ((i + 1) % C::STEPS == 0 && tile + ST < j.tiles) mma_commit(one, &v_empty[tile % ST]);
         };
         // K and V tiles are waited for at their first steps
         auto keys_in = [&](int i) {
@@ -646,10 +657,13 @@ __global__ void __launch_bounds__(kThreads, 1) paged_prefill_kernel(AttnArgs a, 
         for (int i = 0; i < n && ok; ++i) {
           const int tile = tile_of(i, mt);
           if (i % C::STEPS == 0 && !wait(&v_full[tile % ST], (tile / ST) & 1)) break;
-          if (i + 2 < n && !keys_in(i + 2)) break;          // there before the weights are
+          // the next keys are there before the weights are, but for a set with one
+          // place for its keys
+          if (!dual && i + 2 < n && !keys_in(i + 2)) break;
           if (!wait(&p_full[mt * 2 + (i & 1)], (i >> 1) & 1)) break;
           tmem_fence_after();
           values(i);
+          if (dual && i + 2 < n && !keys_in(i + 2)) break;
           // the buffer is free once that product has read it, which is before
           // the next one of this thread writes it
           if (i + 2 < n) scores(i + 2);
@@ -700,49 +714,55 @@ __global__ void __launch_bounds__(kThreads, 1) paged_prefill_kernel(AttnArgs a, 
 }
 
 // ---------------------------------------------------------------------------
-// Join the splits of a tile's rows: a warp per row.
+// Join the splits of a tile's rows: a warp has 8 rows' 32 channels, so that the
+// rows of a unit are read and the units of a row written next to one another.
 // ---------------------------------------------------------------------------
+template <int D>
+constexpr int kJoinRows = 2048 / D;                // rows of a thread block of 8 warps
+
 template <int D, int FMT>
-__global__ void __launch_bounds__(256) paged_prefill_join_kernel(AttnArgs a, int nsplit) {
+__global__ void __launch_bounds__(256) paged_prefill_join_kernel(AttnArgs a, int whole, int nsplit) {
   using C = Prefill<D>;
-  constexpr int DPL = D / 32, PERTILE = C::ROWS / 8;
-  const int lane = threadIdx.x & 31;
-  const int64_t tile = blockIdx.x / PERTILE;
-  const int r = static_cast<int>(blockIdx.x % PERTILE) * 8 + (threadIdx.x >> 5);
-  const int64_t items = a.total_q * a.R / C::ROWS + a.c.B, item = items - 1 - tile / a.c.Hkv;
+  constexpr int PERTILE = C::ROWS / kJoinRows<D>;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int64_t split_tile = blockIdx.x / PERTILE, tile = whole + split_tile;
+  const int r = static_cast<int>(blockIdx.x % PERTILE) * kJoinRows<D> + warp / (D / 32) * 8 + (lane & 7);
+  const int unit = warp % (D / 32) * 8 + (lane >> 3);         // and unit + 4
+  const int64_t items = (a.total_q * a.R >> C::LOG_ROWS) + a.c.B, item = items - 1 - tile / a.c.Hkv;
   const int kvh = static_cast<int>(tile % a.c.Hkv);
   const Found at = find_sequence(a.cu, nullptr, a.c.B, item, a.R, C::LOG_ROWS, 1, lane);
   const int64_t k = at.item, c0 = at.c0, c1 = at.c1, row = k * C::ROWS + r;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   if (c0 < 0 || c1 < c0 || c1 > a.total_q || k < 0 || row >= (c1 - c0) * a.R) return;
-  float o[DPL], m = -INFINITY, l = 0.0f;
+  float o[8], m = -INFINITY, l = 0.0f;
 #pragma unroll
-  for (int i = 0; i < DPL; ++i) o[i] = 0.0f;
-  const float* p = a.part + (tile * nsplit * C::ROWS + r) * (D + 4);
+  for (int i = 0; i < 8; ++i) o[i] = 0.0f;
+  const float* p = a.part + split_tile * nsplit * C::PART;
 #pragma unroll 4
-  for (int s = 0; s < nsplit; ++s, p += C::ROWS * (D + 4)) {
-    const float2 x = *reinterpret_cast<const float2*>(p + D);
+  for (int s = 0; s < nsplit; ++s, p += C::PART) {
+    const float2 x = *reinterpret_cast<const float2*>(p + D * C::ROWS + 2 * r);
+    const float4 y0 = *reinterpret_cast<const float4*>(p + (unit * C::ROWS + r) * 4);
+    const float4 y1 = *reinterpret_cast<const float4*>(p + ((unit + 4) * C::ROWS + r) * 4);
     const float now = fmaxf(m, x.x), ref = now == -INFINITY ? 0.0f : now;
     const float e0 = exp2_approx(m - ref), e1 = exp2_approx(x.x - ref);
     l = l * e0 + x.y * e1;
+    const float y[8] = {y0.x, y0.y, y0.z, y0.w, y1.x, y1.y, y1.z, y1.w};
 #pragma unroll
-    for (int i = 0; i < DPL; i += 2) {
-      const float2 y = *reinterpret_cast<const float2*>(p + lane * DPL + i);
-      o[i] = o[i] * e0 + y.x * e1;
-      o[i + 1] = o[i + 1] * e0 + y.y * e1;
-    }
+    for (int i = 0; i < 8; ++i) o[i] = o[i] * e0 + y[i] * e1;
     m = now;
   }
   const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-  uint16_t* out = a.out + ((c0 + row / a.R) * a.c.Hkv * a.R + kvh * a.R + row % a.R) * D + lane * DPL;
+  uint16_t* out = a.out + ((c0 + row / a.R) * a.c.Hkv * a.R + kvh * a.R + row % a.R) * D + unit * 4;
 #pragma unroll
-  for (int i = 0; i < DPL; i += 2)
-    *reinterpret_cast<uint32_t*>(out + i) = a.bf16 ? pack2<true>(o[i] * inv, o[i + 1] * inv)
-                                                   : pack2<false>(o[i] * inv, o[i + 1] * inv);
+  for (int i = 0; i < 2; ++i) {
+    const float x0 = o[4 * i] * inv, x1 = o[4 * i + 1] * inv, x2 = o[4 * i + 2] * inv, x3 = o[4 * i + 3] * inv;
+    *reinterpret_cast<uint2*>(out + 16 * i) = a.bf16 ? make_uint2(pack2<true>(x0, x1), pack2<true>(x2, x3))
+                                                     : make_uint2(pack2<false>(x0, x1), pack2<false>(x2, x3));
+  }
 }
 
 template <int D, int FMT>
-cudaError_t launch(const AttnArgs& a, int nsplit, cudaStream_t st) {
+cudaError_t launch(const AttnArgs& a, int64_t whole, int nsplit, cudaStream_t st) {
   using C = Prefill<D>;
   auto k = paged_prefill_kernel<D, FMT>;
   static std::atomic<int> ready[64];              // the shared-memory opt-in, once per device
@@ -758,12 +778,12 @@ cudaError_t launch(const AttnArgs& a, int nsplit, cudaStream_t st) {
     if (fa.numRegs * kThreads < kRegsNeeded) return cudaErrorInvalidKernelImage;
     if (dev < 64) ready[dev].store(1, std::memory_order_relaxed);
   }
-  const int64_t tiles = (a.total_q * a.R / C::ROWS + a.c.B) * a.c.Hkv;
-  k<<<static_cast<unsigned>(tiles * nsplit), kThreads, C::SMEM, st>>>(a, nsplit);
+  const int64_t split = ((a.total_q * a.R >> C::LOG_ROWS) + a.c.B) * a.c.Hkv - whole;
+  k<<<static_cast<unsigned>(whole + split * nsplit), kThreads, C::SMEM, st>>>(a, static_cast<int>(whole), nsplit);
   e = cudaGetLastError();
   if (e != cudaSuccess || nsplit == 1) return e;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(tiles * (C::ROWS / 8)));
+  cfg.gridDim = dim3(static_cast<unsigned>(split * (C::ROWS / kJoinRows<D>)));
   cfg.blockDim = dim3(256);
   cfg.stream = st;
   cudaLaunchAttribute attr[1];
@@ -771,18 +791,18 @@ cudaError_t launch(const AttnArgs& a, int nsplit, cudaStream_t st) {
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, paged_prefill_join_kernel<D, FMT>, a, nsplit);
+  return cudaLaunchKernelEx(&cfg, paged_prefill_join_kernel<D, FMT>, a, static_cast<int>(whole), nsplit);
 }
 
 }  // namespace
 
-__attribute__((visibility("hidden"))) int kvq_paged_prefill_launch(const AttnArgs& a, int format, int nsplit,
-                                                                   cudaStream_t st, cudaError_t& err) {
+__attribute__((visibility("hidden"))) int kvq_paged_prefill_launch(const AttnArgs& a, int format, int64_t whole,
+                                                                   int nsplit, cudaStream_t st, cudaError_t& err) {
   const bool f8 = format == KVQ_E4M3;
   switch (a.c.D) {
-    case 64: err = f8 ? launch<64, kE4m3>(a, nsplit, st) : launch<64, kInt8>(a, nsplit, st); break;
-    case 128: err = f8 ? launch<128, kE4m3>(a, nsplit, st) : launch<128, kInt8>(a, nsplit, st); break;
-    default: err = f8 ? launch<256, kE4m3>(a, nsplit, st) : launch<256, kInt8>(a, nsplit, st); break;
+    case 64: err = f8 ? launch<64, kE4m3>(a, whole, nsplit, st) : launch<64, kInt8>(a, whole, nsplit, st); break;
+    case 128: err = f8 ? launch<128, kE4m3>(a, whole, nsplit, st) : launch<128, kInt8>(a, whole, nsplit, st); break;
+    default: err = f8 ? launch<256, kE4m3>(a, whole, nsplit, st) : launch<256, kInt8>(a, whole, nsplit, st); break;
   }
   return err == cudaSuccess ? KVQ_OK : KVQ_ERR_LAUNCH;
 }
