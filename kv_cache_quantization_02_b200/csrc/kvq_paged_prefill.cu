@@ -349,47 +349,58 @@ __global__ void __launch_bounds__(kThreads, 1) paged_prefill_kernel(AttnArgs a, 
 
   // ---- the query rows, fp16 with a power of two each, channels in code order:
   // a lane has 8 channels, a row D / 8 lanes, and all loads of a warp are in
-  // flight before the first is used
+  // flight before the first is used.  (Rows of a softmax warp that has none are
+  // left as they are.)
   {
     constexpr int LANES = D / 8, AT_ONCE = 32 / LANES, W = kThreads / 32 * AT_ONCE, N = (C::ROWS + W - 1) / W;
-    const int c = lane % LANES;
+    const int c = lane % LANES, need = min(C::ROWS, (j.count + 31) & ~31);
+    const int tok0 = j.row0 / a.R, head0 = j.row0 - tok0 * a.R;
+    const float per = __frcp_rn(static_cast<float>(a.R));
     uint4 w[N];
 #pragma unroll
     for (int n = 0; n < N; ++n) {
-      const int r = n * W + warp * AT_ONCE + lane / LANES, row = j.row0 + r, tok = row / a.R;
-      const uint16_t* q = a.q + (j.q0 + static_cast<int64_t>(tok)) * a.q_stride +
-                          static_cast<int64_t>(j.kvh * a.R + row - tok * a.R) * D + c * 8;
+      const int r = n * W + warp * AT_ONCE + lane / LANES;
+      // token and head of row r: the quotient is at most one off
+      int x = head0 + r, tok = static_cast<int>(static_cast<float>(x) * per);
+      x -= tok * a.R;
+      if (x < 0) x += a.R, --tok;
+      if (x >= a.R) x -= a.R, ++tok;
+      const uint16_t* q = a.q + (j.q0 + static_cast<int64_t>(tok0 + tok)) * a.q_stride +
+                          static_cast<int64_t>(j.kvh * a.R + x) * D + c * 8;
       w[n] = r < j.count ? __ldg(reinterpret_cast<const uint4*>(q)) : make_uint4(0, 0, 0, 0);
     }
 #pragma unroll
     for (int n = 0; n < N; ++n) {
+      if (n * W + warp * AT_ONCE >= need) break;
       const int r = n * W + warp * AT_ONCE + lane / LANES;
       float u = a.scale;
-      uint32_t h[4] = {w[n].x, w[n].y, w[n].z, w[n].w};
+      uint32_t h[4] = {w[n].x, w[n].y, w[n].z, w[n].w}, sign = a.negative ? 0x80008000u : 0u;
       if (a.bf16) {
-        float2 x[4];
-        float most = 0.0f;
+        // bf16 magnitudes are ordered as their bits are
+        uint32_t most = __vmaxu2(__vmaxu2(h[0] & 0x7fff7fffu, h[1] & 0x7fff7fffu),
+                                 __vmaxu2(h[2] & 0x7fff7fffu, h[3] & 0x7fff7fffu));
+        if constexpr (LANES == 32) {
+          most = __reduce_max_sync(kAll, max(most & 0xffffu, most >> 16));
+        } else {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          x[i] = unpack2<true>(h[i]);
-          most = max3(most, fabsf(x[i].x), fabsf(x[i].y));
+          for (int o = LANES / 2; o > 0; o >>= 1) most = __vmaxu2(most, __shfl_xor_sync(kAll, most, o));
+          most = max(most & 0xffffu, most >> 16);
         }
-#pragma unroll
-        for (int o = LANES / 2; o > 0; o >>= 1) most = fmaxf(most, __shfl_xor_sync(kAll, most, o));
-        const int k = row_exponent(most);
-        const float up = pow2i(k);
+        const int k = row_exponent(__uint_as_float(most << 16));
+        const float up = a.negative ? -pow2i(k) : pow2i(k);
+        sign = 0;
         u *= pow2i(-k);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) h[i] = pack2<false>(x[i].x * up, x[i].y * up);
+        for (int i = 0; i < 4; ++i) {
+          const float2 x = unpack2<true>(h[i]);
+          h[i] = pack2<false>(x.x * up, x.y * up);
+        }
       }
-      const uint32_t sign = a.negative ? 0x80008000u : 0u;
-      if (r < C::ROWS) {
-        const int rr = r & 127;
-        *reinterpret_cast<uint4*>(qs + ((r >> 7) * C::CB + (c >> 3)) * 16384 + rr * 128 + (((c & 7) ^ (rr & 7)) << 4)) =
-            make_uint4(__byte_perm(h[0], h[1], 0x5410) ^ sign, __byte_perm(h[0], h[1], 0x7632) ^ sign,
-                       __byte_perm(h[2], h[3], 0x5410) ^ sign, __byte_perm(h[2], h[3], 0x7632) ^ sign);
-        if (c == 0) unit[r] = u;
-      }
+      const int rr = r & 127;
+      *reinterpret_cast<uint4*>(qs + ((r >> 7) * C::CB + (c >> 3)) * 16384 + rr * 128 + (((c & 7) ^ (rr & 7)) << 4)) =
+          make_uint4(__byte_perm(h[0], h[1], 0x5410) ^ sign, __byte_perm(h[0], h[1], 0x7632) ^ sign,
+                     __byte_perm(h[2], h[3], 0x5410) ^ sign, __byte_perm(h[2], h[3], 0x7632) ^ sign);
+      if (c == 0) unit[r] = u;
     }
   }
   fence_proxy_async();
