@@ -3,6 +3,7 @@
 
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <atomic>
 #include <cmath>
 #include <cstdint>
@@ -348,14 +349,15 @@ int decode_grid(int B, int max_blocks, int Hq, int Hkv, int D, int block, int wi
 int64_t decode_bytes(int grid, int D) { return static_cast<int64_t>(grid) * (2 * 8 * (D + 4) * 4 + 16); }
 
 // Tiles of a prompt call, and the splits of their keys.  A thread block has an
-// SM to itself; n splits take ceil(tiles n / SMs) rounds of a block's fixed
-// cost (about six key tiles' time) and an n-th of the keys, for which half the
-// table's room stands (causal, and tables are seldom full), or the window.  The
-// first `whole` tiles are not split: either none, or, where tiles see about as
-// many keys (a window, or new tokens that are a quarter of the room at most),
-// full rounds of the GPU, so that only what is left for the last round is.
-// With the last round's tiles split, 5 x 256 tokens behind 4000 took 134 us, not
-// 166; a prompt, whose last tiles are short anyhow, would take 48, not 38.
+// SM to itself and a fixed cost of about six key tiles' time; half the table's
+// room (causal, and tables are seldom full) or the window stands for a tile's
+// keys.  Where tiles see about as many keys (a window, or new tokens that are a
+// quarter of the room at most) they take full rounds of the GPU, and those rounds
+// may be left unsplit, so that only what is left for the last one is split: 5 x 256
+// tokens behind 4000 took 134 us then, not 166.  A prompt's tiles see anything
+// from nothing to all, so it takes the longest tile's time or the average load of
+// an SM: 4096 tokens of 8 heads took 66 us with two splits, not 84, and 1500 tokens
+// 38 us without one, 48 with its last round split.
 struct PromptGrid {
   int64_t tiles, whole;
   int nsplit;
@@ -366,26 +368,29 @@ PromptGrid prompt_grid(int B, int max_blocks, int64_t total_q, int Hq, int Hkv, 
   const int rows = D == 256 ? 128 : 256, kt = D == 256 ? 64 : 128;
   PromptGrid g;
   g.tiles = (total_q * (Hq / Hkv) / rows + B) * Hkv;
-  int64_t keys = static_cast<int64_t>(max_blocks) * block / kt / 2;
-  const int64_t seen = (static_cast<int64_t>(window) + rows * Hkv / Hq) / kt + 1, sms = sm_count();
-  if (window > 0 && seen < keys) keys = seen;
+  constexpr double kFixed = 6.0;
+  const int64_t sms = sm_count(), seen = (static_cast<int64_t>(window) + rows * Hkv / Hq) / kt + 1;
+  const double most = static_cast<double>(max_blocks) * block / kt;
+  const double keys = window > 0 && seen < most / 2 ? static_cast<double>(seen) : most / 2;
   const bool alike = window > 0 || total_q * 4 <= static_cast<int64_t>(B) * max_blocks * block;
   const int64_t rounds = alike ? g.tiles / sms : 0, rest = g.tiles % sms;
+  auto cost = [&](int64_t full, int64_t split, int n) {       // `full` rounds, then `split` tiles
+    if (alike) return full * (kFixed + keys) + (split * n + sms - 1) / sms * (kFixed + std::ceil(keys / n));
+    return std::max(kFixed + most / n, split * (kFixed * n + keys) / sms);
+  };
   g.nsplit = 1;
   g.whole = g.tiles;
-  int64_t best = (g.tiles + sms - 1) / sms * (6 + keys) * 16;
-  for (int n = 2; n <= 16 && n <= keys / 2; ++n) {
-    // a sixteenth more must be gained by each further split's partial sums
-    const int64_t each = (6 + (keys + n - 1) / n) * 17;
+  double best = cost(0, g.tiles, 1);
+  for (int n = 2; n <= 16 && n <= keys / 2; ++n)
     for (const int64_t full : {int64_t{0}, rounds}) {
-      const int64_t split = full ? rest : g.tiles;
-      const int64_t cost = full * (6 + keys) * 16 + (split * n + sms - 1) / sms * each;
-      if (split == 0 || split >= 2 * sms || full > 3 || cost >= best) continue;
-      best = cost;
+      const int64_t split = full > 0 ? rest : g.tiles;
+      // a sixteenth more must be gained, which the partial sums cost
+      const double c = cost(full, split, n) * 17 / 16;
+      if (split == 0 || split >= 2 * sms || full > 3 || c >= best) continue;
+      best = c;
       g.nsplit = n;
       g.whole = g.tiles - split;
     }
-  }
   g.bytes = g.nsplit > 1 ? (g.tiles - g.whole) * g.nsplit * rows * (D + 2) * 4 : 0;
   return g;
 }
