@@ -373,6 +373,12 @@ PromptGrid prompt_grid(int B, int max_blocks, int64_t total_q, int Hq, int Hkv, 
   const double most = static_cast<double>(max_blocks) * block / kt;
   const double keys = window > 0 && seen < most / 2 ? static_cast<double>(seen) : most / 2;
   const bool alike = window > 0 || total_q * 4 <= static_cast<int64_t>(B) * max_blocks * block;
+  if (alike && g.tiles <= sms && keys >= 4 && B <= 32) {      // one piece a thread block, by the lengths
+    g.whole = -1;
+    g.nsplit = static_cast<int>(sms);
+    g.bytes = sms * rows * (D + 2) * 4;
+    return g;
+  }
   const int64_t rounds = alike ? g.tiles / sms : 0, rest = g.tiles % sms;
   auto cost = [&](int64_t full, int64_t split, int n) {       // `full` rounds, then `split` tiles
     if (alike) return full * (kFixed + keys) + (split * n + sms - 1) / sms * (kFixed + std::ceil(keys / n));

@@ -38,6 +38,7 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <atomic>
 #include <cstdint>
 #include <type_traits>
@@ -178,51 +179,144 @@ struct Job {
   int lo, hi;                 // keys that some row sees
   int first, tiles, steps;    // first key of the first tile; tiles and steps of this split
   int split, nsplit;
-  int64_t tile;               // of a split tile: its number among them, for partial sums
+  int64_t part;               // a piece's number, for its partial sums
 };
+
+// The keys lo .. hi - 1 that rows row0 .. row0 + count - 1 of a sequence see,
+// the first key of their first tile and the number of tiles.
+struct Span {
+  int lo, hi, first, tiles;
+};
+template <int D>
+__device__ __forceinline__ Span span_of(const AttnArgs& a, int L, int n, int row0, int count) {
+  using C = Prefill<D>;
+  const int p0 = L - n + row0 / a.R, p1 = L - n + (row0 + count - 1) / a.R;
+  Span x;
+  x.lo = a.window > 0 ? max(0, p0 - a.window + 1) : 0;
+  x.hi = max(0, p1 + 1);
+  x.first = x.lo / C::KT * C::KT;
+  x.tiles = x.hi > x.lo ? (x.hi - x.first + C::KT - 1) / C::KT : 0;
+  return x;
+}
+
+// The splits of a call whose tiles fit the GPU at once, from the lengths (up to
+// 32 sequences, one a lane): every tile of a sequence is split alike, into pieces
+// of about as many key tiles as the shortest that still let all pieces start at
+// once.  Pieces are numbered sequence by sequence, last tiles first.
+struct Plan {
+  int c0, n, L;                                   // a lane's sequence: first row of q, tokens, length
+  int tiles, ns;                                  // its row tiles, the pieces of each
+  int pieces, before;                             // all its pieces, those of the sequences before it
+};
+constexpr int kPlanned = -1;                      // instead of the number of unsplit tiles
+
+template <int D>
+__device__ __forceinline__ Plan make_plan(const AttnArgs& a, int places, int lane, unsigned& bad) {
+  using C = Prefill<D>;
+  Plan p;
+  const bool mine = lane < a.c.B;
+  const int c0 = mine ? a.cu[lane] : 0, c1 = mine ? a.cu[lane + 1] : 0, len = mine ? a.seq_len[lane] : 0;
+  const bool wrong = c0 < 0 || c1 < c0 || c1 > a.total_q;
+  if (wrong) bad |= kFaultLength;
+  p.c0 = c0;
+  p.n = wrong ? 0 : c1 - c0;
+  p.L = p.n > 0 ? clamped_length(a, len, bad) : 0;
+  const int rows = p.n * a.R;                     // total_q R is an int
+  p.tiles = ((rows + C::ROWS - 1) >> C::LOG_ROWS) * a.c.Hkv;
+  // the key tiles of its longest row tile, at most (a window's may begin and end inside one)
+  int keys = rows > 0 ? (p.L + C::KT - 1) / C::KT : 0;
+  if (a.window > 0) keys = min(static_cast<int64_t>(keys), (a.window + int64_t{C::ROWS} / a.R) / C::KT + 2);
+  const float all = static_cast<float>(__reduce_add_sync(kAll, p.tiles));
+  float work = static_cast<float>(p.tiles) * static_cast<float>(keys);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) work += __shfl_xor_sync(kAll, work, o);
+  const int most = __reduce_max_sync(kAll, keys);
+  auto pieces_of = [&](int per) { return max(1, (keys + per - 1) / per); };
+  // bisection between the average load and what surely fits: pieces are at most
+  // work / per + tiles
+  int lo = max(2, static_cast<int>(work / static_cast<float>(places))), hi = most;
+  if (all < static_cast<float>(places))
+    hi = static_cast<int>(fminf(static_cast<float>(hi), work / (static_cast<float>(places) - all) + 1.0f));
+  lo = min(lo, hi);
+#pragma unroll 1
+  while (lo < hi) {
+    const int per = lo + (hi - lo) / 2;
+    const int64_t mine_all = static_cast<int64_t>(p.tiles) * pieces_of(per);
+    const int sum = __reduce_add_sync(kAll, static_cast<int>(min(mine_all, int64_t{1} << 20)));
+    if (sum <= places) hi = per;
+    else lo = per + 1;
+  }
+  p.ns = most > hi + 2 ? pieces_of(max(hi, 1)) : 1;         // what joining costs
+  if (__reduce_add_sync(kAll, static_cast<int>(min(static_cast<int64_t>(p.tiles) * p.ns, int64_t{1} << 20))) > places)
+    p.ns = 1;
+  p.pieces = p.tiles * p.ns;
+  p.before = p.pieces;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int x = __shfl_up_sync(kAll, p.before, o);
+    if (lane >= o) p.before += x;
+  }
+  p.before -= p.pieces;
+  return p;
+}
 
 template <int D>
 __device__ __forceinline__ bool find_job(const AttnArgs& a, int whole, int nsplit, Job& j, unsigned& bad) {
   using C = Prefill<D>;
   unsigned x = blockIdx.x;
-  j.split = 0;
-  j.nsplit = 1;
-  if (x >= static_cast<unsigned>(whole)) {
-    x -= static_cast<unsigned>(whole);
-    j.nsplit = nsplit;
-    j.split = static_cast<int>(x % static_cast<unsigned>(nsplit));
-    x /= static_cast<unsigned>(nsplit);
-    j.tile = x;
-    x += static_cast<unsigned>(whole);
+  int k;
+  if (whole == kPlanned) {
+    const int lane = threadIdx.x & 31;
+    const Plan p = make_plan<D>(a, gridDim.x, lane, bad);
+    const int at = static_cast<int>(x), b = __ffs(__ballot_sync(kAll, at - p.before < p.pieces && at >= p.before)) - 1;
+    bad = __reduce_or_sync(kAll, bad);
+    if (b < 0) return false;
+    j.b = b;
+    j.q0 = __shfl_sync(kAll, p.c0, b);
+    j.n = __shfl_sync(kAll, p.n, b);
+    j.L = __shfl_sync(kAll, p.L, b);
+    j.nsplit = __shfl_sync(kAll, p.ns, b);
+    const int y = at - __shfl_sync(kAll, p.before, b), z = y / j.nsplit;
+    j.split = y - z * j.nsplit;
+    j.kvh = z % a.c.Hkv;
+    k = __shfl_sync(kAll, p.tiles, b) / a.c.Hkv - 1 - z / a.c.Hkv;
+    j.part = at;
+  } else {
+    j.split = 0;
+    j.nsplit = 1;
+    j.part = 0;
+    if (x >= static_cast<unsigned>(whole)) {
+      x -= static_cast<unsigned>(whole);
+      j.part = x;
+      j.nsplit = nsplit;
+      j.split = static_cast<int>(x % static_cast<unsigned>(nsplit));
+      x = x / static_cast<unsigned>(nsplit) + static_cast<unsigned>(whole);
+    }
+    j.kvh = static_cast<int>(x % static_cast<unsigned>(a.c.Hkv));
+    // the last tiles of a sequence see most keys: they start first
+    const int64_t items = (a.total_q * a.R >> C::LOG_ROWS) + a.c.B;
+    const int64_t item = items - 1 - x / static_cast<unsigned>(a.c.Hkv);
+    const Found f = find_sequence(a.cu, a.seq_len, a.c.B, item, a.R, C::LOG_ROWS, 1, threadIdx.x & 31);
+    j.b = f.b;
+    const int64_t c0 = f.c0, c1 = f.c1;
+    if (c0 < 0 || c1 < c0 || c1 > a.total_q) {
+      bad |= kFaultLength;
+      return false;
+    }
+    j.n = static_cast<int>(c1 - c0);
+    j.q0 = static_cast<int>(c0);
+    if (f.item < 0 || f.item * C::ROWS >= (c1 - c0) * a.R) return false;
+    k = static_cast<int>(f.item);
+    j.L = clamped_length(a, f.more, bad);
   }
-  j.kvh = static_cast<int>(x % static_cast<unsigned>(a.c.Hkv));
-  // the last tiles of a sequence see most keys: they start first
-  const int64_t items = (a.total_q * a.R >> C::LOG_ROWS) + a.c.B;
-  const int64_t item = items - 1 - x / static_cast<unsigned>(a.c.Hkv);
-  const Found f = find_sequence(a.cu, a.seq_len, a.c.B, item, a.R, C::LOG_ROWS, 1, threadIdx.x & 31);
-  j.b = f.b;
-  const int64_t k = f.item, c0 = f.c0, c1 = f.c1;
-  if (c0 < 0 || c1 < c0 || c1 > a.total_q) {
-    bad |= kFaultLength;
-    return false;
-  }
-  j.n = static_cast<int>(c1 - c0);
-  j.q0 = static_cast<int>(c0);
-  const int64_t rows = (c1 - c0) * a.R;
-  if (k < 0 || k * C::ROWS >= rows) return false;
-  j.row0 = static_cast<int>(k * C::ROWS);
-  j.count = static_cast<int>(min(static_cast<int64_t>(C::ROWS), rows - j.row0));
-  j.L = clamped_length(a, f.more, bad);
-  const int p0 = j.L - j.n + j.row0 / a.R, p1 = j.L - j.n + (j.row0 + j.count - 1) / a.R;
-  j.lo = a.window > 0 ? max(0, p0 - a.window + 1) : 0;
-  j.hi = max(0, p1 + 1);
-  j.first = j.lo / C::KT * C::KT;
-  const int tiles = j.hi > j.lo ? (j.hi - j.first + C::KT - 1) / C::KT : 0;
-  // (tiles < 2^25 and nsplit <= 16)
-  const int t0 = static_cast<int>(static_cast<unsigned>(tiles * j.split) / static_cast<unsigned>(j.nsplit));
-  const int t1 = static_cast<int>(static_cast<unsigned>(tiles * (j.split + 1)) / static_cast<unsigned>(j.nsplit));
-  j.first += t0 * C::KT;
-  j.tiles = t1 - t0;
+  j.row0 = k * C::ROWS;
+  j.count = min(C::ROWS, j.n * a.R - j.row0);
+  const Span s = span_of<D>(a, j.L, j.n, j.row0, j.count);
+  j.lo = s.lo;
+  j.hi = s.hi;
+  const int each = s.tiles / j.nsplit, more = s.tiles - each * j.nsplit;      // the first pieces have one more
+  j.first = s.first + (each * j.split + min(j.split, more)) * C::KT;
+  j.tiles = each + (j.split < more ? 1 : 0);
   j.steps = j.tiles > 0 ? min(j.tiles * C::STEPS, (j.hi - j.first + kStep - 1) / kStep) : 0;
   return true;
 }
@@ -300,6 +394,9 @@ __global__ void __launch_bounds__(kThreads, 1) paged_prefill_kernel(AttnArgs a, 
   uint32_t* shared_word = reinterpret_cast<uint32_t*>(bars + C::NBAR);         // the tensor memory's address
 
   const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(kAll, tid >> 5, 0);
+  // the joining kernel's thread blocks may take their places as soon as all of
+  // these have theirs; they wait for this grid's end
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   unsigned bad = 0;
   Job j;
   if (!find_job<D>(a, whole, nsplit, j, bad)) {
@@ -568,7 +665,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_prefill_kernel(AttnArgs a, 
         // the first set writes
       } else if (ok && j.nsplit > 1) {
         // unit by unit (four channels), all rows of a unit next to one another
-        float* part = a.part + (j.tile * j.nsplit + j.split) * C::PART;
+        float* part = a.part + j.part * C::PART;
 #pragma unroll 1
         for (int c = 0; c < D / 32; ++c) {
           uint32_t o[32];
@@ -732,23 +829,52 @@ template <int D>
 constexpr int kJoinRows = 2048 / D;                // rows of a thread block of 8 warps
 
 template <int D, int FMT>
-__global__ void __launch_bounds__(256) paged_prefill_join_kernel(AttnArgs a, int whole, int nsplit) {
+__global__ void __launch_bounds__(256) paged_prefill_join_kernel(AttnArgs a, int whole, int nsplit, int places) {
   using C = Prefill<D>;
   constexpr int PERTILE = C::ROWS / kJoinRows<D>;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int64_t split_tile = blockIdx.x / PERTILE, tile = whole + split_tile;
   const int r = static_cast<int>(blockIdx.x % PERTILE) * kJoinRows<D> + warp / (D / 32) * 8 + (lane & 7);
   const int unit = warp % (D / 32) * 8 + (lane >> 3);         // and unit + 4
-  const int64_t items = (a.total_q * a.R >> C::LOG_ROWS) + a.c.B, item = items - 1 - tile / a.c.Hkv;
-  const int kvh = static_cast<int>(tile % a.c.Hkv);
-  const Found at = find_sequence(a.cu, nullptr, a.c.B, item, a.R, C::LOG_ROWS, 1, lane);
-  const int64_t k = at.item, c0 = at.c0, c1 = at.c1, row = k * C::ROWS + r;
+  int64_t tile = blockIdx.x / PERTILE, piece, c0, n, k;
+  int kvh;
+  if (whole == kPlanned) {
+    unsigned bad = 0;
+    const Plan p = make_plan<D>(a, places, lane, bad);
+    const int mine = p.ns > 1 ? p.tiles : 0;      // only these have anything to join
+    int before = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int x = __shfl_up_sync(kAll, before, o);
+      if (lane >= o) before += x;
+    }
+    before -= mine;
+    const int at = static_cast<int>(tile), b = __ffs(__ballot_sync(kAll, at >= before && at - before < mine)) - 1;
+    if (b < 0) return;
+    nsplit = __shfl_sync(kAll, p.ns, b);
+    const int z = at - __shfl_sync(kAll, before, b);
+    c0 = __shfl_sync(kAll, p.c0, b);
+    n = __shfl_sync(kAll, p.n, b);
+    piece = __shfl_sync(kAll, p.before, b) + z * nsplit;
+    kvh = z % a.c.Hkv;
+    k = __shfl_sync(kAll, p.tiles, b) / a.c.Hkv - 1 - z / a.c.Hkv;
+  } else {
+    piece = tile * nsplit;
+    tile += whole;
+    const int64_t items = (a.total_q * a.R >> C::LOG_ROWS) + a.c.B, item = items - 1 - tile / a.c.Hkv;
+    kvh = static_cast<int>(tile % a.c.Hkv);
+    const Found at = find_sequence(a.cu, nullptr, a.c.B, item, a.R, C::LOG_ROWS, 1, lane);
+    c0 = at.c0;
+    n = at.c1 - c0;
+    k = at.item;
+    if (c0 < 0 || n < 0 || at.c1 > a.total_q || k < 0) return;
+  }
+  const int64_t row = k * C::ROWS + r;
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  if (c0 < 0 || c1 < c0 || c1 > a.total_q || k < 0 || row >= (c1 - c0) * a.R) return;
+  if (row >= n * a.R) return;
   float o[8], m = -INFINITY, l = 0.0f;
 #pragma unroll
   for (int i = 0; i < 8; ++i) o[i] = 0.0f;
-  const float* p = a.part + split_tile * nsplit * C::PART;
+  const float* p = a.part + piece * C::PART;
 #pragma unroll 4
   for (int s = 0; s < nsplit; ++s, p += C::PART) {
     const float2 x = *reinterpret_cast<const float2*>(p + D * C::ROWS + 2 * r);
@@ -789,8 +915,10 @@ cudaError_t launch(const AttnArgs& a, int64_t whole, int nsplit, cudaStream_t st
     if (fa.numRegs * kThreads < kRegsNeeded) return cudaErrorInvalidKernelImage;
     if (dev < 64) ready[dev].store(1, std::memory_order_relaxed);
   }
-  const int64_t split = ((a.total_q * a.R >> C::LOG_ROWS) + a.c.B) * a.c.Hkv - whole;
-  k<<<static_cast<unsigned>(whole + split * nsplit), kThreads, C::SMEM, st>>>(a, static_cast<int>(whole), nsplit);
+  const int64_t tiles = ((a.total_q * a.R >> C::LOG_ROWS) + a.c.B) * a.c.Hkv;
+  const int64_t split = whole == kPlanned ? std::min<int64_t>(tiles, nsplit / 2) : tiles - whole;
+  const unsigned grid = static_cast<unsigned>(whole == kPlanned ? nsplit : whole + split * nsplit);
+  k<<<grid, kThreads, C::SMEM, st>>>(a, static_cast<int>(whole), nsplit);
   e = cudaGetLastError();
   if (e != cudaSuccess || nsplit == 1) return e;
   cudaLaunchConfig_t cfg = {};
@@ -802,7 +930,8 @@ cudaError_t launch(const AttnArgs& a, int64_t whole, int nsplit, cudaStream_t st
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, paged_prefill_join_kernel<D, FMT>, a, static_cast<int>(whole), nsplit);
+  return cudaLaunchKernelEx(&cfg, paged_prefill_join_kernel<D, FMT>, a, static_cast<int>(whole), nsplit,
+                            static_cast<int>(grid));
 }
 
 }  // namespace
