@@ -373,7 +373,7 @@ PromptGrid prompt_grid(int B, int max_blocks, int64_t total_q, int Hq, int Hkv, 
   const double most = static_cast<double>(max_blocks) * block / kt;
   const double keys = window > 0 && seen < most / 2 ? static_cast<double>(seen) : most / 2;
   const bool alike = window > 0 || total_q * 4 <= static_cast<int64_t>(B) * max_blocks * block;
-  if (alike && g.tiles <= sms && keys >= 4 && B <= 32) {      // one piece a thread block, by the lengths
+  if (alike && g.tiles <= 4 * sms && keys >= 4 && B <= 32) {  // by the lengths, on the device
     g.whole = -1;
     g.nsplit = static_cast<int>(sms);
     g.bytes = sms * rows * (D + 2) * 4;

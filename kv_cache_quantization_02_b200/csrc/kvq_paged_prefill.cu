@@ -77,7 +77,7 @@ struct Prefill {
   static constexpr int PART = ROWS * (D + 2);     // floats of a tile's partial sums, references and sums of weights
   static constexpr int META = 4 * NSUB * 16;      // scales of four tiles
   static constexpr int NBAR = 4 * STAGES + 4 + 3 * 4 + 1;
-  static constexpr int SMEM = 1024 + QBYTES + 2 * STAGES * TILE + META + ROWS * 4 + 128 * 8 + NBAR * 8 + 64;
+  static constexpr int SMEM = 1024 + QBYTES + 2 * STAGES * TILE + META + ROWS * 4 + 128 * 8 + NBAR * 8 + 8 + 80;
   // tensor memory columns: two score buffers (the weights over them) for each
   // 128 rows, then the outputs
   static constexpr int O0 = MT * 2 * kStep;
@@ -180,6 +180,7 @@ struct Job {
   int first, tiles, steps;    // first key of the first tile; tiles and steps of this split
   int split, nsplit;
   int64_t part;               // a piece's number, for its partial sums
+  bool there;                 // there is work for this thread block
 };
 
 // The keys lo .. hi - 1 that rows row0 .. row0 + count - 1 of a sequence see,
@@ -199,16 +200,33 @@ __device__ __forceinline__ Span span_of(const AttnArgs& a, int L, int n, int row
   return x;
 }
 
-// The splits of a call whose tiles fit the GPU at once, from the lengths (up to
-// 32 sequences, one a lane): every tile of a sequence is split alike, into pieces
-// of about as many key tiles as the shortest that still let all pieces start at
-// once.  Pieces are numbered sequence by sequence, last tiles first.
+// The splits of a call from its lengths (up to 32 sequences, one a lane).  Where
+// all tiles fit the GPU at once, every tile of a sequence is split alike, into
+// pieces of about as many key tiles as the shortest that still let all pieces
+// start at once.  Where they do not, full rounds are left whole and what is left
+// over is split to fill one more.  Tiles are numbered sequence by sequence, last
+// tiles first, and pieces in the order of their tiles.
 struct Plan {
   int c0, n, L;                                   // a lane's sequence: first row of q, tokens, length
   int tiles, ns;                                  // its row tiles, the pieces of each
-  int pieces, before;                             // all its pieces, those of the sequences before it
-};
-constexpr int kPlanned = -1;                      // instead of the number of unsplit tiles
+  int pieces, before, tiles_before;               // all its pieces; those, and the tiles, of the sequences before it
+  int whole, rest, rest_ns;                       // tiles before any split one (0: the lanes' ns hold), tiles after them,
+};                                                // the pieces of each
+__device__ __forceinline__ int sum_before(int x, int lane) {
+  int y = x;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int z = __shfl_up_sync(kAll, y, o);
+    if (lane >= o) y += z;
+  }
+  return y - x;
+}
+// The lane whose `mine` numbers from `before` on hold x, or -1.
+__device__ __forceinline__ int lane_of(int x, int before, int mine) {
+  return __ffs(__ballot_sync(kAll, x >= before && x - before < mine)) - 1;
+}
+constexpr int kPlanned = -1;                      // instead of the number of unsplit tiles; the splits are then the
+                                                  // thread blocks that run at once
 
 template <int D>
 __device__ __forceinline__ Plan make_plan(const AttnArgs& a, int places, int lane, unsigned& bad) {
@@ -226,11 +244,22 @@ __device__ __forceinline__ Plan make_plan(const AttnArgs& a, int places, int lan
   // the key tiles of its longest row tile, at most (a window's may begin and end inside one)
   int keys = rows > 0 ? (p.L + C::KT - 1) / C::KT : 0;
   if (a.window > 0) keys = min(static_cast<int64_t>(keys), (a.window + int64_t{C::ROWS} / a.R) / C::KT + 2);
-  const float all = static_cast<float>(__reduce_add_sync(kAll, p.tiles));
+  p.tiles_before = sum_before(p.tiles, lane);
+  const int most = __reduce_max_sync(kAll, keys), total = __reduce_add_sync(kAll, p.tiles);
+  p.whole = p.rest = 0;
+  p.rest_ns = p.ns = 1;
+  p.pieces = p.tiles;
+  p.before = p.tiles_before;
+  if (total > places) {
+    p.rest = total % places;
+    p.whole = total - p.rest;
+    if (p.rest > 0) p.rest_ns = max(1, min(places / p.rest, most / 2));
+    return p;
+  }
+  const float all = static_cast<float>(total);
   float work = static_cast<float>(p.tiles) * static_cast<float>(keys);
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) work += __shfl_xor_sync(kAll, work, o);
-  const int most = __reduce_max_sync(kAll, keys);
   auto pieces_of = [&](int per) { return max(1, (keys + per - 1) / per); };
   // bisection between the average load and what surely fits: pieces are at most
   // work / per + tiles
@@ -246,19 +275,17 @@ __device__ __forceinline__ Plan make_plan(const AttnArgs& a, int places, int lan
     if (sum <= places) hi = per;
     else lo = per + 1;
   }
-  p.ns = most > hi + 2 ? pieces_of(max(hi, 1)) : 1;         // what joining costs
-  if (__reduce_add_sync(kAll, static_cast<int>(min(static_cast<int64_t>(p.tiles) * p.ns, int64_t{1} << 20))) > places)
-    p.ns = 1;
-  p.pieces = p.tiles * p.ns;
-  p.before = p.pieces;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int x = __shfl_up_sync(kAll, p.before, o);
-    if (lane >= o) p.before += x;
-  }
-  p.before -= p.pieces;
+  if (most <= hi + 2) return p;                   // what joining costs
+  const int ns = pieces_of(max(hi, 1));
+  if (__reduce_add_sync(kAll, static_cast<int>(min(static_cast<int64_t>(p.tiles) * ns, int64_t{1} << 20))) > places)
+    return p;
+  p.ns = ns;
+  p.pieces = p.tiles * ns;
+  p.before = sum_before(p.pieces, lane);
   return p;
 }
+
+static_assert(sizeof(Job) <= 80, "its place in shared memory");
 
 template <int D>
 __device__ __forceinline__ bool find_job(const AttnArgs& a, int whole, int nsplit, Job& j, unsigned& bad) {
@@ -267,20 +294,37 @@ __device__ __forceinline__ bool find_job(const AttnArgs& a, int whole, int nspli
   int k;
   if (whole == kPlanned) {
     const int lane = threadIdx.x & 31;
-    const Plan p = make_plan<D>(a, gridDim.x, lane, bad);
-    const int at = static_cast<int>(x), b = __ffs(__ballot_sync(kAll, at - p.before < p.pieces && at >= p.before)) - 1;
+    const Plan p = make_plan<D>(a, nsplit, lane, bad);
     bad = __reduce_or_sync(kAll, bad);
+    const int at = static_cast<int>(x);
+    int z;                                        // the tile's number in its sequence
+    if (p.whole > 0) {
+      const int y = max(at - p.whole, 0), t = y / p.rest_ns;
+      j.nsplit = at < p.whole ? 1 : p.rest_ns;
+      j.split = y - t * p.rest_ns;
+      z = min(at, p.whole) + t;
+      j.part = y;
+      if (t > 0 && t >= p.rest) return false;
+    } else {
+      z = at;
+      j.part = at;
+    }
+    const int b = p.whole > 0 ? lane_of(z, p.tiles_before, p.tiles) : lane_of(at, p.before, p.pieces);
     if (b < 0) return false;
+    if (p.whole > 0) {
+      z -= __shfl_sync(kAll, p.tiles_before, b);
+    } else {
+      const int y = at - __shfl_sync(kAll, p.before, b);
+      j.nsplit = __shfl_sync(kAll, p.ns, b);
+      z = y / j.nsplit;
+      j.split = y - z * j.nsplit;
+    }
     j.b = b;
     j.q0 = __shfl_sync(kAll, p.c0, b);
     j.n = __shfl_sync(kAll, p.n, b);
     j.L = __shfl_sync(kAll, p.L, b);
-    j.nsplit = __shfl_sync(kAll, p.ns, b);
-    const int y = at - __shfl_sync(kAll, p.before, b), z = y / j.nsplit;
-    j.split = y - z * j.nsplit;
     j.kvh = z % a.c.Hkv;
     k = __shfl_sync(kAll, p.tiles, b) / a.c.Hkv - 1 - z / a.c.Hkv;
-    j.part = at;
   } else {
     j.split = 0;
     j.nsplit = 1;
@@ -392,17 +436,25 @@ __global__ void __launch_bounds__(kThreads, 1) paged_prefill_kernel(AttnArgs a, 
   uint64_t *meta_full = bars + 4 * ST, *s_full = meta_full + 4, *p_full = s_full + 4, *o_full = p_full + 4;
   uint64_t* joined = o_full + 4;
   uint32_t* shared_word = reinterpret_cast<uint32_t*>(bars + C::NBAR);         // the tensor memory's address
+  Job* job = reinterpret_cast<Job*>(shared_word + 2);
 
   const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(kAll, tid >> 5, 0);
   // the joining kernel's thread blocks may take their places as soon as all of
   // these have theirs; they wait for this grid's end
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   unsigned bad = 0;
-  Job j;
-  if (!find_job<D>(a, whole, nsplit, j, bad)) {
-    if (bad && tid == 0) atomicOr(&g_prefill_fault, bad);
-    return;
+  if (warp == 0) {                                // one warp finds the work for all
+    Job found;
+    const bool there = find_job<D>(a, whole, nsplit, found, bad);
+    if (lane == 0) {
+      found.there = there;
+      *job = found;
+    }
+    if (!there && bad && lane == 0) atomicOr(&g_prefill_fault, bad);
   }
+  __syncthreads();
+  if (!job->there) return;
+  const Job j = *job;
 
   if (warp == kIssuer) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;"
@@ -829,7 +881,7 @@ template <int D>
 constexpr int kJoinRows = 2048 / D;                // rows of a thread block of 8 warps
 
 template <int D, int FMT>
-__global__ void __launch_bounds__(256) paged_prefill_join_kernel(AttnArgs a, int whole, int nsplit, int places) {
+__global__ void __launch_bounds__(256) paged_prefill_join_kernel(AttnArgs a, int whole, int nsplit) {
   using C = Prefill<D>;
   constexpr int PERTILE = C::ROWS / kJoinRows<D>;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -839,22 +891,26 @@ __global__ void __launch_bounds__(256) paged_prefill_join_kernel(AttnArgs a, int
   int kvh;
   if (whole == kPlanned) {
     unsigned bad = 0;
-    const Plan p = make_plan<D>(a, places, lane, bad);
-    const int mine = p.ns > 1 ? p.tiles : 0;      // only these have anything to join
-    int before = mine;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int x = __shfl_up_sync(kAll, before, o);
-      if (lane >= o) before += x;
+    const Plan p = make_plan<D>(a, nsplit, lane, bad);
+    const int at = static_cast<int>(tile);
+    int b, z;
+    if (p.whole > 0) {
+      if (p.rest_ns == 1 || at >= p.rest) return;
+      b = lane_of(p.whole + at, p.tiles_before, p.tiles);
+      if (b < 0) return;
+      z = p.whole + at - __shfl_sync(kAll, p.tiles_before, b);
+      nsplit = p.rest_ns;
+      piece = static_cast<int64_t>(at) * nsplit;
+    } else {
+      const int mine = p.ns > 1 ? p.tiles : 0, before = sum_before(mine, lane);      // only these have anything to join
+      b = lane_of(at, before, mine);
+      if (b < 0) return;
+      z = at - __shfl_sync(kAll, before, b);
+      nsplit = __shfl_sync(kAll, p.ns, b);
+      piece = __shfl_sync(kAll, p.before, b) + z * nsplit;
     }
-    before -= mine;
-    const int at = static_cast<int>(tile), b = __ffs(__ballot_sync(kAll, at >= before && at - before < mine)) - 1;
-    if (b < 0) return;
-    nsplit = __shfl_sync(kAll, p.ns, b);
-    const int z = at - __shfl_sync(kAll, before, b);
     c0 = __shfl_sync(kAll, p.c0, b);
     n = __shfl_sync(kAll, p.n, b);
-    piece = __shfl_sync(kAll, p.before, b) + z * nsplit;
     kvh = z % a.c.Hkv;
     k = __shfl_sync(kAll, p.tiles, b) / a.c.Hkv - 1 - z / a.c.Hkv;
   } else {
@@ -916,8 +972,10 @@ cudaError_t launch(const AttnArgs& a, int64_t whole, int nsplit, cudaStream_t st
     if (dev < 64) ready[dev].store(1, std::memory_order_relaxed);
   }
   const int64_t tiles = ((a.total_q * a.R >> C::LOG_ROWS) + a.c.B) * a.c.Hkv;
+  // (a planned call's nsplit: the places, all thread blocks that run at once)
   const int64_t split = whole == kPlanned ? std::min<int64_t>(tiles, nsplit / 2) : tiles - whole;
-  const unsigned grid = static_cast<unsigned>(whole == kPlanned ? nsplit : whole + split * nsplit);
+  const unsigned grid = static_cast<unsigned>(whole != kPlanned ? whole + split * nsplit
+                                              : tiles <= nsplit ? nsplit : (tiles / nsplit + 1) * nsplit);
   k<<<grid, kThreads, C::SMEM, st>>>(a, static_cast<int>(whole), nsplit);
   e = cudaGetLastError();
   if (e != cudaSuccess || nsplit == 1) return e;
@@ -930,8 +988,7 @@ cudaError_t launch(const AttnArgs& a, int64_t whole, int nsplit, cudaStream_t st
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, paged_prefill_join_kernel<D, FMT>, a, static_cast<int>(whole), nsplit,
-                            static_cast<int>(grid));
+  return cudaLaunchKernelEx(&cfg, paged_prefill_join_kernel<D, FMT>, a, static_cast<int>(whole), nsplit);
 }
 
 }  // namespace
