@@ -223,6 +223,50 @@ def test_prefill(kvq, D, Hkv, R, block, fmt, dtype, ctx, new, window):
     check(unsplit[:c.n], want, bound)
 
 
+# Few queries over long sequences: the keys of a tile are split by the lengths.
+MIXES = [
+    # 32 sequences, some without new tokens, some without any before them; 33 are split without the lengths
+    (64, 2, 3, 16, "e4m3", "bf16", [97 * i % 1700 if i % 5 else 0 for i in range(32)], [i * 7 % 10 for i in range(32)]),
+    (64, 2, 3, 16, "e4m3", "bf16", [97 * i % 1700 if i % 5 else 0 for i in range(33)], [i * 7 % 10 for i in range(33)]),
+    (128, 1, 8, 64, "int8", "fp16", [9000, 40, 0], [1, 33, 2]),
+    (128, 3, 2, 128, "e4m3", "fp16", [5000], [300]),
+    # more tiles than thread blocks run at once: only those that are left over are split
+    (256, 16, 1, 32, "int8", "bf16", [1500, 1300, 1700], [500, 400, 257]),
+]
+
+
+@pytest.mark.parametrize("D,Hkv,R,block,fmt,dtype,ctx,new", MIXES)
+@pytest.mark.parametrize("window", [0, 600])
+def test_prefill_split_by_lengths(kvq, D, Hkv, R, block, fmt, dtype, ctx, new, window):
+    test_prefill(kvq, D, Hkv, R, block, fmt, dtype, ctx, new, window)
+
+
+def test_prefill_lengths_change_between_replays(kvq):
+    """A captured call splits by the lengths of each replay."""
+    c = Case(128, 2, 32, "int8", [1500, 20, 900], [10, 120, 70], seed=21, R=4)
+    q = c.rows(8, "fp16")
+    d, qd = c.cuda(), q.cuda()
+    cu, lens = d.cu.clone(), d.seq_len.clone()
+    out = torch.zeros_like(qd)
+    run = lambda: kvq.paged_attention_prefill(qd, cu, lens, d.table, *d.cache(), sm_scale=0.1, out=out)
+    run()
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        run()
+    n = c.n
+    for offsets, lengths in (([0, 10, 130, 200], [1510, 140, 970]), ([0, 200, 200, 200], [1510, 140, 970]),
+                             ([0, 1, 2, 3], [1510, 33, 500]), ([0, 0, 140, 140], [0, 140, 0])):
+        cu.copy_(torch.tensor(offsets, dtype=torch.int32))
+        lens.copy_(torch.tensor(lengths, dtype=torch.int32))
+        out.fill_(7.0)
+        g.replay()
+        want, bound = c.attend(q[:offsets[-1]], torch.tensor(offsets, dtype=torch.int32),
+                               torch.tensor(lengths, dtype=torch.int32), 0.1)
+        check(out[:offsets[-1]], want, bound)
+        assert n == 200 and bool((out[offsets[-1]:] == 7.0).all())
+
+
 @pytest.mark.parametrize("D,block", [(64, 16), (128, 64), (256, 32)])
 def test_queries_without_keys(kvq, D, block):
     """More queries than positions: the first ones stand before the sequence and give zeros; so do empty sequences."""
