@@ -349,15 +349,21 @@ int decode_grid(int B, int max_blocks, int Hq, int Hkv, int D, int block, int wi
 int64_t decode_bytes(int grid, int D) { return static_cast<int64_t>(grid) * (2 * 8 * (D + 4) * 4 + 16); }
 
 // Tiles of a prompt call, and the splits of their keys.  A thread block has an
-// SM to itself and a fixed cost of about six key tiles' time; half the table's
-// room (causal, and tables are seldom full) or the window stands for a tile's
-// keys.  Where tiles see about as many keys (a window, or new tokens that are a
-// quarter of the room at most) they take full rounds of the GPU, and those rounds
-// may be left unsplit, so that only what is left for the last one is split: 5 x 256
-// tokens behind 4000 took 134 us then, not 166.  A prompt's tiles see anything
-// from nothing to all, so it takes the longest tile's time or the average load of
-// an SM: 4096 tokens of 8 heads took 66 us with two splits, not 84, and 1500 tokens
-// 38 us without one, 48 with its last round split.
+// SM to itself and a fixed cost of about six key tiles' time.
+//
+// Tiles see about as many keys where there is a window, or where the new tokens
+// are a quarter of the table's room at most.  Up to 32 sequences are then split by
+// their lengths, on the device (make_plan in kvq_paged_prefill.cu): whole = -1, and
+// nsplit the thread blocks that run at once.  More sequences take full rounds of
+// the GPU at half the room's keys (tables are seldom full) or the window's, and
+// those rounds may be left unsplit, so that only what is left for the last one is
+// split.  Without either, 5 x 256 tokens behind 4000 took 166 us; with the last round
+// split 134, by the lengths 114.
+//
+// A prompt's tiles see anything from nothing to all, so it takes the longest
+// tile's time or the average load of an SM: 4096 tokens of 8 heads took 66 us with
+// two splits, not 84, and 1500 tokens 38 us without one, 48 with its last round
+// split.
 struct PromptGrid {
   int64_t tiles, whole;
   int nsplit;

@@ -7,7 +7,8 @@
 //
 // Work.  The query heads of a KV head share its keys, so the rows of a tile
 // are (token, head) pairs of one KV head, R rows a token, packed across token
-// boundaries: 2 x 128 rows a thread block (128 at D = 256).  Where the tiles do
+// boundaries: 2 x 128 rows a thread block (128 at D = 256).  Up to 128 rows
+// share their key tiles out over both sets of warps instead.  Where the tiles do
 // not fill the GPU the keys of a tile are split over several thread blocks,
 // whose partial sums a second kernel joins.
 //
@@ -29,8 +30,8 @@
 // The reference of a row's softmax moves rarely (kLazy), and only then is O
 // rescaled in tensor memory, by the thread that owns the row.
 //
-// Measured at D = 128, 32 query heads on 8: a prompt of 8192 tokens 0.61 ms (900
-// TFLOP/s), of 16384 (16 on 4) 1005.  A key tile takes 4,150 cycles: 2,048 of the
+// Measured at D = 128, 32 query heads on 8: a prompt of 8192 tokens 0.60 ms (916
+// TFLOP/s), of 16384 (16 on 4) 1030; 8 x 32 tokens behind 8192 77 us.  A key tile takes 4,150 cycles: 2,048 of the
 // exponential unit, about 2,500 of the tensor cores, the rest latencies.  With
 // one score buffer of 128 keys for each 128 rows (larger MMAs, but the softmax
 // waits for them) it was 0.72 ms, with sixteen softmax warps 0.64 ms.
