@@ -377,45 +377,51 @@ __device__ __forceinline__ int part_row(const AttnArgs& a, const Job& j, int key
   return id < 0 ? -1 : (id * a.c.Hkv + j.kvh) * a.c.block + (key & (a.c.block - 1));
 }
 
-// One of four warps' share of a tile's codes: chunks of 256 codes (32 lanes of
-// 8), chunk 4 i + which for i < N.  Chunk 4 i + which lies in part
-// 4 i / (D / 16), since which < 4, and parts that are not there become zeros.
+// One of four warps' share of a tile's codes: chunks of 512 codes (32 lanes of
+// 16), chunk 4 i + which for i < N; parts that are not there become zeros.  (With
+// loads of 8 codes a lane, asking for a tile took a converter's 1,100 cycles.)
 template <int D>
 struct Share {
   using C = Prefill<D>;
-  static constexpr int N = C::KT * D / 1024;
-  static constexpr int PERPART = D / 16;          // chunks of a 16-key part
-  uint2 w[N];
+  static constexpr int N = C::KT * D / 2048;
+  static constexpr int PERPART = D / 32;          // chunks of a 16-key part
+  uint4 w[N];
   // (e4m3: keys from `live` on, behind the sequence's last, as zeros)
   template <int FMT>
   __device__ __forceinline__ void load(const uint8_t* codes, int rows, int live, int which, int lane) {
-    const uint8_t* mine = codes + which * 256 + lane * 8;
+    const uint8_t* mine = codes + which % PERPART * 512 + lane * 16;
     const uint8_t* p = nullptr;
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-      if (4 * i % PERPART == 0) {                 // a part's first chunk
-        const int row = __shfl_sync(kAll, rows, 4 * i / PERPART);
+      if (4 * i % PERPART == 0) {                 // a part's first chunk for this warp
+        const int row = __shfl_sync(kAll, rows, 4 * i / PERPART + which / PERPART);
         p = row < 0 ? nullptr : mine + static_cast<int64_t>(row) * D;
       }
-      const bool there = p != nullptr && (FMT == kInt8 || ((4 * i + which) * 32 + lane) / (D / 8) < live);
-      w[i] = there ? __ldg(reinterpret_cast<const uint2*>(p + 4 * i % PERPART * 256)) : make_uint2(0, 0);
+      const bool there = p != nullptr && (FMT == kInt8 || ((4 * i + which) * 32 + lane) / (D / 16) < live);
+      w[i] = there ? __ldg(reinterpret_cast<const uint4*>(p + 4 * i % PERPART * 512)) : make_uint4(0, 0, 0, 0);
     }
   }
   // To the tile at dst: row r, 8-channel unit c at unit (c mod 8) ^ (r mod 8) of
-  // row r of block c / 8.  From one chunk to the next the row grows by 1024 / D,
-  // which changes r mod 8 at D = 256 only, by 4.
+  // row r of block c / 8.  A lane has units c and c + 1, c even, and r mod 8 is the
+  // same for all its chunks.  Eight lanes store at once, which have all even units of
+  // one row's two blocks (D > 64): those of odd blocks begin with unit c + 1.
   template <int FMT>
   __device__ __forceinline__ void store(uint32_t dst, int which, int lane) const {
-    const int x = which * 32 + lane, r = x / (D / 8), c = x % (D / 8);
-    const uint32_t at = dst + (c >> 3) * (C::KT * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4);
+    const int x = which * 32 + lane, r = x / (D / 16), c = x % (D / 16) * 2;
+    const bool odd = D > 64 && (c >> 3 & 1);
+    const uint32_t at = dst + (c >> 3) * (C::KT * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4) ^ (odd ? 16u : 0u);
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-      uint32_t h[4];
-      codes_to_half2<FMT>(w[i].x, h[0], h[1]);
-      codes_to_half2<FMT>(w[i].y, h[2], h[3]);
-      const uint32_t to = (D == 256 && (i & 1) ? at ^ 64u : at) + i * (1024 / D * 128);
-      asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" :: "r"(to), "r"(h[0]), "r"(h[1]), "r"(h[2]), "r"(h[3])
-                   : "memory");
+      const uint32_t to = at + i * (2048 / D * 128);
+      const uint32_t v[4] = {odd ? w[i].z : w[i].x, odd ? w[i].w : w[i].y, odd ? w[i].x : w[i].z, odd ? w[i].y : w[i].w};
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        uint32_t h[4];
+        codes_to_half2<FMT>(v[2 * k], h[0], h[1]);
+        codes_to_half2<FMT>(v[2 * k + 1], h[2], h[3]);
+        asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};"
+                     :: "r"(k == 0 ? to : to ^ 16u), "r"(h[0]), "r"(h[1]), "r"(h[2]), "r"(h[3]) : "memory");
+      }
     }
   }
 };
@@ -463,7 +469,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_prefill_kernel(AttnArgs a, 
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
   // Up to 128 rows: the second set of softmax warps takes the odd key tiles of
-  // the same rows, and the two sets' sums are joined in the end.  (Stage 1 of the
+  // the same rows, and the two sets' sums are joined in the end.  (Place 1 of the
   // tiles in shared memory is then the second set's alone.)
   const int sets = C::MT == 2 && j.count > 128 ? 2 : 1;
   const bool dual = C::MT == 2 && sets == 1;
@@ -673,26 +679,16 @@ __global__ void __launch_bounds__(kThreads, 1) paged_prefill_kernel(AttnArgs a, 
       // ---- outputs
       if (steps > 0 && wait(&o_full[mt * 2 + ((steps - 1) & 1)], ((steps - 1) >> 1) & 1)) tmem_fence_after();
       const bool some = steps > 0 && ok;
-      // The second set leaves its sums in stage 1 of K and V, column by column.
-      auto spare = [&](int c) {
-        return reinterpret_cast<float*>((c < D / 2 ? kbuf : vbuf) + C::TILE) + (c % (D / 2)) * 128 + own;
-      };
       const bool joins = dual && mt == 0 && steps_of(1) > 0;
       float f0 = 1.0f, f1 = 0.0f;
       if (dual && mt == 1 && some) {
-#pragma unroll 1
-        for (int c = 0; c < D; c += 32) {
-          uint32_t o[32];
-          tmem_ld32(o, o_at + c);
-          tmem_wait_ld();
-#pragma unroll
-          for (int e = 0; e < 32; ++e) spare(c)[e * 128] = __uint_as_float(o[e]);
-        }
         second[own] = make_float2(M, l);
+        tmem_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(joined);
       }
       if (joins && wait(joined, 0)) {
+        tmem_fence_after();
         const float2 x = second[own];
         const float now = fmaxf(M, x.x), ref = now == -INFINITY ? 0.0f : now;
         f0 = exp2_approx(M - ref);
@@ -708,9 +704,13 @@ __global__ void __launch_bounds__(kThreads, 1) paged_prefill_kernel(AttnArgs a, 
 #pragma unroll
           for (int e = 0; e < 32; ++e) o[e] = 0;
         }
-        if (joins) {
+        if (joins) {                                        // the second set's are in the same lanes
+          uint32_t o2[32];
+          tmem_ld32(o2, o_at + D + c);
+          tmem_wait_ld();
 #pragma unroll
-          for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f0 + spare(c)[e * 128] * f1);
+          for (int e = 0; e < 32; ++e)
+            o[e] = __float_as_uint(__uint_as_float(o[e]) * f0 + __uint_as_float(o2[e]) * f1);
         }
       };
       const float inv = l == 0.0f ? 0.0f : 1.0f / l;
