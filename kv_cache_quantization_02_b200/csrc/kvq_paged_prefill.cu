@@ -888,32 +888,29 @@ __global__ void __launch_bounds__(256) paged_prefill_join_kernel(AttnArgs a, int
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int r = static_cast<int>(blockIdx.x % PERTILE) * kJoinRows<D> + warp / (D / 32) * 8 + (lane & 7);
   const int unit = warp % (D / 32) * 8 + (lane >> 3);         // and unit + 4
-  int64_t tile = blockIdx.x / PERTILE, piece, c0, n, k;
-  int kvh;
+  int64_t tile = blockIdx.x / PERTILE, piece = 0, c0 = 0, n = 0, k = 0;          // n = 0: nothing to join
+  int kvh = 0;
   if (whole == kPlanned) {
     unsigned bad = 0;
     const Plan p = make_plan<D>(a, nsplit, lane, bad);
     const int at = static_cast<int>(tile);
     int b, z;
     if (p.whole > 0) {
-      if (p.rest_ns == 1 || at >= p.rest) return;
-      b = lane_of(p.whole + at, p.tiles_before, p.tiles);
-      if (b < 0) return;
-      z = p.whole + at - __shfl_sync(kAll, p.tiles_before, b);
+      b = p.rest_ns == 1 || at >= p.rest ? -1 : lane_of(p.whole + at, p.tiles_before, p.tiles);
+      z = p.whole + at - __shfl_sync(kAll, p.tiles_before, b & 31);
       nsplit = p.rest_ns;
       piece = static_cast<int64_t>(at) * nsplit;
     } else {
-      const int mine = p.ns > 1 ? p.tiles : 0, before = sum_before(mine, lane);      // only these have anything to join
+      const int mine = p.ns > 1 ? p.tiles : 0, before = sum_before(mine, lane);
       b = lane_of(at, before, mine);
-      if (b < 0) return;
-      z = at - __shfl_sync(kAll, before, b);
-      nsplit = __shfl_sync(kAll, p.ns, b);
-      piece = __shfl_sync(kAll, p.before, b) + z * nsplit;
+      z = at - __shfl_sync(kAll, before, b & 31);
+      nsplit = __shfl_sync(kAll, p.ns, b & 31);
+      piece = __shfl_sync(kAll, p.before, b & 31) + z * nsplit;
     }
-    c0 = __shfl_sync(kAll, p.c0, b);
-    n = __shfl_sync(kAll, p.n, b);
+    c0 = __shfl_sync(kAll, p.c0, b & 31);
+    n = b < 0 ? 0 : __shfl_sync(kAll, p.n, b & 31);
     kvh = z % a.c.Hkv;
-    k = __shfl_sync(kAll, p.tiles, b) / a.c.Hkv - 1 - z / a.c.Hkv;
+    k = __shfl_sync(kAll, p.tiles, b & 31) / a.c.Hkv - 1 - z / a.c.Hkv;
   } else {
     piece = tile * nsplit;
     tile += whole;
@@ -921,13 +918,16 @@ __global__ void __launch_bounds__(256) paged_prefill_join_kernel(AttnArgs a, int
     kvh = static_cast<int>(tile % a.c.Hkv);
     const Found at = find_sequence(a.cu, nullptr, a.c.B, item, a.R, C::LOG_ROWS, 1, lane);
     c0 = at.c0;
-    n = at.c1 - c0;
+    n = c0 < 0 || at.c1 > a.total_q || at.item < 0 ? 0 : at.c1 - c0;
     k = at.item;
-    if (c0 < 0 || n < 0 || at.c1 > a.total_q || k < 0) return;
   }
   const int64_t row = k * C::ROWS + r;
+  const bool none = n == 0 || row < 0 || row >= n * a.R;
+  // This grid's end stands for the first one's, so one thread block waits for that
+  // even if it has nothing to do.
+  if (none && blockIdx.x > 0) return;
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  if (row >= n * a.R) return;
+  if (none) return;
   float o[8], m = -INFINITY, l = 0.0f;
 #pragma unroll
   for (int i = 0; i < 8; ++i) o[i] = 0.0f;
