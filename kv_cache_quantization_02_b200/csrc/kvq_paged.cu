@@ -378,7 +378,7 @@ PromptGrid prompt_grid(int B, int max_blocks, int64_t total_q, int Hq, int Hkv, 
   const int64_t sms = sm_count(), seen = (static_cast<int64_t>(window) + rows * Hkv / Hq) / kt + 1;
   const double most = static_cast<double>(max_blocks) * block / kt;
   const double keys = window > 0 && seen < most / 2 ? static_cast<double>(seen) : most / 2;
-  const bool alike = window > 0 || total_q * 4 <= static_cast<int64_t>(B) * max_blocks * block;
+  const bool alike = (window > 0 && seen < most / 2) || total_q * 4 <= static_cast<int64_t>(B) * max_blocks * block;
   if (alike && g.tiles <= 4 * sms && keys >= 4 && B <= 32) {  // by the lengths, on the device
     g.whole = -1;
     g.nsplit = static_cast<int>(sms);
@@ -479,7 +479,7 @@ int attention_args(AttnArgs& p, const void* q, int dtype, int64_t q_stride, cons
   if (rc != KVQ_OK) return rc;
   p.q = nullptr;
   if (Hq < Hkv || Hq % Hkv != 0 || total_q < 0 || total_q > INT32_MAX || total_q * Hq > INT32_MAX || window < 0 ||
-      !std::isfinite(sm_scale))
+      !std::isfinite(sm_scale * 1.4426951f))      // (the scale the kernels use)
     return KVQ_ERR_COUNT;
   rc = check_stride(q_stride, Hq, D);
   if (rc != KVQ_OK) return rc;
@@ -494,7 +494,9 @@ int attention_args(AttnArgs& p, const void* q, int dtype, int64_t q_stride, cons
   p.out = static_cast<uint16_t*>(out);
   p.cu = cu_q; p.seq_len = seq_len; p.part = nullptr;
   p.q_stride = q_stride; p.total_q = total_q;
-  p.R = Hq / Hkv; p.window = window; p.bf16 = dtype == KVQ_BF16; p.negative = sm_scale < 0.0f;
+  p.R = Hq / Hkv; p.bf16 = dtype == KVQ_BF16; p.negative = sm_scale < 0.0f;
+  // (a window of the whole table is none, and differences with one then fit an int)
+  p.window = window < static_cast<int64_t>(max_blocks) * block ? window : 0;
   p.scale = static_cast<float>(std::fabs(static_cast<double>(sm_scale)) * 1.4426950408889634);
   return KVQ_OK;
 }

@@ -241,6 +241,21 @@ def test_prefill_split_by_lengths(kvq, D, Hkv, R, block, fmt, dtype, ctx, new, w
     test_prefill(kvq, D, Hkv, R, block, fmt, dtype, ctx, new, window)
 
 
+def test_the_largest_window(kvq):
+    """A window beyond the table is none, also for queries that stand before their sequence."""
+    c = Case(128, 2, 32, "int8", [1300, 0], [40, 30], seed=22, R=2)
+    lens = torch.tensor([1340, 10], dtype=torch.int32)
+    q = c.rows(4, "fp16")
+    d = c.cuda()
+    for window in (2**31 - 1, c.table.shape[1] * 32):
+        args = (q.cuda(), d.cu, lens.cuda(), d.table, *d.cache())
+        want, bound = c.attend(q, c.cu, lens, 0.1)
+        check(kvq.paged_attention_prefill(*args, sm_scale=0.1, window=window), want, bound)
+        check(kvq.paged_attention_prefill(*args, sm_scale=0.1, window=window, workspace=False), want, bound)
+        want, bound = c.attend(q[:2], range(3), lens, 0.1)
+        check(kvq.paged_attention_decode(q[:2].cuda(), *args[2:], sm_scale=0.1, window=window), want, bound)
+
+
 def test_prefill_lengths_change_between_replays(kvq):
     """A captured call splits by the lengths of each replay."""
     c = Case(128, 2, 32, "int8", [1500, 20, 900], [10, 120, 70], seed=21, R=4)

@@ -93,6 +93,12 @@ def test_write_and_read(kvq):
     assert _write(kvq, B=1 << 29, Hkv=1) == -5     # more work items than a grid has
 
 
+def test_a_scale_beyond_fp32(kvq):
+    """The kernels use sm_scale log2(e), which has to be finite too."""
+    for prefill in (False, True):
+        assert _attend(kvq, prefill, scale=3e38) == -5 and _attend(kvq, prefill, scale=-3e38) == -5
+
+
 def test_attention(kvq):
     for prefill in (False, True):
         f = lambda **kw: _attend(kvq, prefill, **kw)
