@@ -57,7 +57,7 @@ def build_torch_module() -> str:
            *(f"-I{d}" for d in includes), TORCH_SOURCE, "-o", TORCH_MODULE,
            f"-L{PKG}", "-l:libkvq.so", "-Wl,-rpath,$ORIGIN",
            *(f"-L{d}" for d in cpp_extension.library_paths()),
-           "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda"]
+           "-ltorch_python", "-ltorch_cpu", "-ltorch_cuda", "-lc10", "-lc10_cuda"]
     res = subprocess.run(cmd, capture_output=True, text=True)
     if res.returncode != 0:
         raise RuntimeError("g++ failed:\n" + res.stdout + res.stderr)

@@ -11,7 +11,7 @@
 #include <Python.h>
 
 #include <ATen/core/Tensor.h>
-#include <ATen/ops/empty.h>
+#include <ATen/cuda/EmptyTensor.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
@@ -121,17 +121,23 @@ struct Rows {
   }
 };
 
-at::Tensor output(PyObject* given, at::IntArrayRef shape, const at::Tensor& like, at::ScalarType type, int index,
-                  const char* name) {
-  if (given == Py_None) return at::empty(shape, like.options().dtype(type));
+// A new tensor on the current device, straight from the caching allocator (the
+// dispatcher takes as long again, and a read of a few rows makes two of them).
+at::Tensor fresh(at::IntArrayRef shape, at::ScalarType type, int index) {
+  return at::Tensor(at::detail::empty_cuda(shape, type, at::Device(at::kCUDA, static_cast<c10::DeviceIndex>(index)),
+                                           std::nullopt));
+}
+
+at::Tensor output(PyObject* given, at::IntArrayRef shape, at::ScalarType type, int index, const char* name) {
+  if (given == Py_None) return fresh(shape, type, index);
   const at::Tensor& t = tensor(given, name);
   need(t, type, shape, index, name);
   return t;
 }
 
 // True: a new one of `bytes`; a uint8 tensor: that; anything else: none.
-at::Tensor workspace(PyObject* given, int64_t bytes, const at::Tensor& like, int index) {
-  if (given == Py_True) return bytes > 0 ? at::empty({bytes}, like.options().dtype(at::kByte)) : at::Tensor();
+at::Tensor workspace(PyObject* given, int64_t bytes, int index) {
+  if (given == Py_True) return bytes > 0 ? fresh(at::IntArrayRef(&bytes, 1), at::kByte, index) : at::Tensor();
   if (!THPVariable_Check(given)) return at::Tensor();
   const at::Tensor& t = THPVariable_Unpack(given);
   const int64_t n = t.numel();
@@ -203,8 +209,8 @@ PyObject* paged_read(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const at::ScalarType type = dtype == KVQ_BF16 ? at::kBFloat16 : at::kHalf;
     const int64_t shape[3] = {tokens, c.Hkv, c.D};
     const c10::cuda::CUDAGuard guard(static_cast<c10::DeviceIndex>(c.index));
-    at::Tensor k = output(a[9], shape, c.kc, type, c.index, "k_out");
-    at::Tensor v = output(a[10], shape, c.kc, type, c.index, "v_out");
+    at::Tensor k = output(a[9], shape, type, c.index, "k_out");
+    at::Tensor v = output(a[10], shape, type, c.index, "v_out");
     const int rc = kvq_paged_read(cu, start, c.table_ptr(), c.B, c.max_blocks, tokens, c.Hkv, c.D, c.block, c.format,
                                   c.num_blocks, c.kc.const_data_ptr(), c.vc.const_data_ptr(),
                                   static_cast<const float*>(c.ks.const_data_ptr()),
@@ -233,10 +239,10 @@ PyObject* paged_attention_decode(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const int window = as_int(a[8]);
     const int64_t shape[3] = {r.n, r.heads, c.D};
     const c10::cuda::CUDAGuard guard(static_cast<c10::DeviceIndex>(c.index));
-    at::Tensor out = output(a[9], shape, q, q.scalar_type(), c.index, "out");
+    at::Tensor out = output(a[9], shape, q.scalar_type(), c.index, "out");
     const at::Tensor ws = workspace(
         a[10], a[10] == Py_True ? kvq_paged_decode_workspace_bytes(c.B, c.max_blocks, r.heads, c.Hkv, c.D, c.block, window)
-                                : 0, q, c.index);
+                                : 0, c.index);
     const int rc = kvq_paged_attention_decode(
         q.const_data_ptr(), r.dtype, r.stride, lens, c.table_ptr(), c.B, c.max_blocks, r.heads, c.Hkv, c.D, c.block,
         c.format, c.num_blocks, c.kc.const_data_ptr(), c.vc.const_data_ptr(),
@@ -259,11 +265,11 @@ PyObject* paged_attention_prefill(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const int window = as_int(a[9]);
     const int64_t shape[3] = {r.n, r.heads, c.D};
     const c10::cuda::CUDAGuard guard(static_cast<c10::DeviceIndex>(c.index));
-    at::Tensor out = output(a[10], shape, q, q.scalar_type(), c.index, "out");
+    at::Tensor out = output(a[10], shape, q.scalar_type(), c.index, "out");
     const at::Tensor ws = workspace(a[11], a[11] == Py_True ? kvq_paged_prefill_workspace_bytes(
                                                                   c.B, c.max_blocks, r.n, r.heads, c.Hkv, c.D, c.block,
                                                                   window)
-                                                            : 0, q, c.index);
+                                                            : 0, c.index);
     const int rc = kvq_paged_attention_prefill(
         q.const_data_ptr(), r.dtype, r.stride, cu, lens, c.table_ptr(), c.B, c.max_blocks, r.n, r.heads, c.Hkv, c.D,
         c.block, c.format, c.num_blocks, c.kc.const_data_ptr(), c.vc.const_data_ptr(),
