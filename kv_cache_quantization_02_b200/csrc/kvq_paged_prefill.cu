@@ -31,7 +31,7 @@
 // rescaled in tensor memory, by the thread that owns the row.
 //
 // Measured at D = 128, 32 query heads on 8: a prompt of 8192 tokens 0.60 ms (916
-// TFLOP/s), of 16384 (16 on 4) 1030; 8 x 32 tokens behind 8192 77 us.  A key tile takes 4,150 cycles: 2,048 of the
+// TFLOP/s), of 16384 (16 on 4) 1030; 8 x 32 tokens behind 8192 74 us.  A key tile takes 4,150 cycles: 2,048 of the
 // exponential unit, about 2,500 of the tensor cores, the rest latencies.  With
 // one score buffer of 128 keys for each 128 rows (larger MMAs, but the softmax
 // waits for them) it was 0.72 ms, with sixteen softmax warps 0.64 ms.
