@@ -678,6 +678,36 @@ def test_bad_tables_and_lengths(kvq):
     assert all(same(x, y) for x, y in zip(before, d.cache()))
 
 
+@pytest.mark.parametrize("B", [3, 33])                  # split by the lengths, and without them
+def test_bad_lengths_and_offsets_of_long_sequences(kvq, B):
+    ctx, new = [2000, 1500, 40] + [3] * (B - 3), [9, 20, 30] + [0] * (B - 3)
+    c = Case(64, 2, 64, "int8", ctx, new, seed=23, R=2)
+    q = c.rows(4, "fp16")
+    c.table = c.table.clamp(min=0)
+    d = c.cuda()
+    run = lambda cu, lens: kvq.paged_attention_prefill(
+        q.cuda(), torch.tensor(cu, dtype=torch.int32).cuda(), lens.cuda(), d.table, *d.cache(), sm_scale=0.1,
+        out=torch.full_like(q, 7.0).cuda())
+    rest = [3] * (B - 3)
+    lens = torch.tensor([2009, 10 ** 9, -5] + rest, dtype=torch.int32)
+    clamped = torch.tensor([2009, c.table.shape[1] * 64, 0] + rest, dtype=torch.int32)
+    want, bound = c.attend(q, c.cu, clamped, 0.1)
+    check(run(c.cu.tolist(), lens), want, bound)
+    assert kvq.kvq_fault_status(clear=True) == 8
+    want, bound = c.attend(q, c.cu, c.seq_len, 0.1)
+    end = [59] * (B - 3)
+    for cu, right in (([0, 9, 10 ** 6, 59], range(0, 9)), ([-5, 9, 29, 59], range(9, 59))):
+        got = run(cu + end, c.seq_len)
+        assert kvq.kvq_fault_status(clear=True) == 8
+        check(got[right.start:right.stop], want[right.start:right.stop], bound[right.start:right.stop])
+        assert all(bool((got[i] == 7.0).all()) for i in range(59) if i not in right)
+    # sequences that share rows: whichever is last, those of one alone are right
+    got = run([0, 59, 9, 59] + end, c.seq_len)
+    assert kvq.kvq_fault_status(clear=True) == 8
+    want, bound = c.attend(q, torch.tensor([0, 59, 59, 59] + end, dtype=torch.int32), c.seq_len, 0.1)
+    check(got[:9], want[:9], bound[:9])
+
+
 def test_empty_calls(kvq):
     c = Case(128, 2, 16, "int8", [], [], seed=20, extra=4)
     d = c.cuda()
