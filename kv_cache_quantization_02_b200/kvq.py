@@ -12,7 +12,9 @@ The raw entry points keep the C names and take integer device addresses:
 with torch when none are given, call the C entry point on the current (or
 given) stream and raise ``KvqError`` on a non-zero status.  Every step of the
 computation runs in the library's CUDA kernels; there is no fallback.  If the
-library is missing, importing this module raises ImportError.
+library is missing, importing this module raises ImportError; if _kvq_torch.so,
+the torch side of the paged cache's calls, is missing or made for another
+torch, the first of those calls does.
 """
 from __future__ import annotations
 
@@ -504,7 +506,19 @@ def _paged_module():
     return module
 
 
-_paged = _paged_module()
+class _Paged:
+    """The compiled calls, loaded at the first of them (each is then an
+    attribute of its own): _kvq_torch.so is made for one build of torch, and
+    the codec needs libkvq.so alone."""
+
+    def __getattr__(self, name):
+        module = _paged_module()
+        for call in ("paged_write", "paged_read", "paged_attention_decode", "paged_attention_prefill"):
+            setattr(self, call, getattr(module, call))
+        return getattr(module, name)
+
+
+_paged = _Paged()
 
 
 def _paged_result(result):
