@@ -414,7 +414,7 @@ int kvq_paged_read(const int32_t *cu_tokens, const int32_t *start, const int32_t
  *               slower.  Calls that may overlap in time need one each.
  * The codes enter the products exactly, scores and sums are fp32, the softmax
  * weights are fp16 values (relative rounding 2^-11) in the value product.
- * Scales are read as max(scale, 2^-40).
+ * Key and value scales are read as max(scale, 2^-40), a NaN as 2^-40.
  */
 int kvq_paged_attention_decode(const void *q, int dtype, int64_t q_stride, const int32_t *seq_len,
                                const int32_t *block_table, int B, int max_blocks, int Hq, int Hkv,

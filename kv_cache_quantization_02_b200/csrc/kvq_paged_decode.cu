@@ -379,6 +379,8 @@ __global__ void __launch_bounds__(kWarps * 32, kDecodeBlocks<D>) paged_decode_ke
       if (fresh) {                                // the scales' loads had the copies' issue to arrive in
         fresh = false;
         const float v0 = fmaxf(sv0, kScaleMin), v1 = fmaxf(sv1, kScaleMin);
+        sk0 = fmaxf(sk0, kScaleMin);
+        sk1 = fmaxf(sk1, kScaleMin);
         sv0 = id0 >= 0 ? log2f(v0) : -INFINITY;   // no block: weights 0
         sv1 = id1 >= 0 ? log2f(v1) : -INFINITY;
         iv0 = id0 >= 0 ? __frcp_rn(v0) : 0.0f;

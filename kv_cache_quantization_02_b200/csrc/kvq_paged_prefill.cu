@@ -847,7 +847,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_prefill_kernel(AttnArgs a, 
         if (warp == kFirstK && rows >= 0) {
           const int x = rows >> a.c.log_block;
           const float v = fmaxf(a.c.vs[x], kScaleMin);
-          m4 = make_float4(a.c.ks[x], log2f(v), __frcp_rn(v), 0.0f);
+          m4 = make_float4(fmaxf(a.c.ks[x], kScaleMin), log2f(v), __frcp_rn(v), 0.0f);
         }
         if (i >= ST && !wait(&empty[st], (i / ST - 1) & 1)) break;
         if (warp == kFirstK) {

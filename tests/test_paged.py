@@ -781,3 +781,23 @@ def test_wrong_tensors(kvq):
 
 def test_formats_are_named(kvq):
     assert set(FORMATS.values()) == set(QMAX)
+
+
+@pytest.mark.parametrize("D,block,fmt", [(64, 16, "int8"), (128, 32, "e4m3"), (256, 16, "int8"), (128, 16, "int8")])
+def test_scales_that_no_write_makes(kvq, D, block, fmt):
+    """A cache that other code filled may hold key and value scales that are NaN, negative, infinite below, zero or
+    tiny: both attentions read max(scale, 2^-40)."""
+    c = Case(D, 1, block, fmt, [0, 3], [170, 90], seed=26, R=2)
+    odd = [math.nan, -0.01, 0.0, -math.inf, 2.0 ** -50]
+    for i, x in enumerate(odd):
+        c.ks[int(c.table[i % 2, i // 2])] = x
+        c.vs[int(c.table[i % 2, (i + 1) // 2 % 3])] = x
+    d = c.cuda()
+    for s in (c.ks, c.vs):
+        s.copy_(torch.nan_to_num(s, nan=0.0).clamp(min=2.0 ** -40))
+    q = c.rows(2, "bf16")
+    for scale in (0.3, -0.3):
+        want, bound = c.attend(q, c.cu, c.seq_len, scale)
+        check(kvq.paged_attention_prefill(q.cuda(), d.cu, d.seq_len, d.table, *d.cache(), sm_scale=scale), want, bound)
+        want, bound = c.attend(q[:2], range(3), c.seq_len, scale)
+        check(kvq.paged_attention_decode(q[:2].cuda(), d.seq_len, d.table, *d.cache(), sm_scale=scale), want, bound)
