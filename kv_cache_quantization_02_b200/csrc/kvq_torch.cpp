@@ -14,6 +14,7 @@
 #include <ATen/cuda/EmptyTensor.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
+#include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <cstdint>
@@ -170,6 +171,8 @@ PyObject* guarded(Py_ssize_t n, Py_ssize_t want, F f) {
     return f();
   } catch (const Wrong& e) {
     if (!PyErr_Occurred()) PyErr_SetString(PyExc_ValueError, e.what());
+  } catch (const c10::Error&) {                   // torch's own class: callers that run out of memory evict blocks
+    if (!PyErr_Occurred()) torch::translate_exception_to_python(std::current_exception());
   } catch (const std::exception& e) {
     if (!PyErr_Occurred()) PyErr_SetString(PyExc_RuntimeError, e.what());
   }

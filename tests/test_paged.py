@@ -801,3 +801,13 @@ def test_scales_that_no_write_makes(kvq, D, block, fmt):
         check(kvq.paged_attention_prefill(q.cuda(), d.cu, d.seq_len, d.table, *d.cache(), sm_scale=scale), want, bound)
         want, bound = c.attend(q[:2], range(3), c.seq_len, scale)
         check(kvq.paged_attention_decode(q[:2].cuda(), d.seq_len, d.table, *d.cache(), sm_scale=scale), want, bound)
+
+
+def test_out_of_memory(kvq):
+    """Outputs that do not fit the GPU raise what torch's own allocations raise, and the next call works."""
+    c = Case(128, 8, 16, "int8", [3], [5], seed=27)
+    d = c.cuda()
+    with pytest.raises(torch.OutOfMemoryError):
+        kvq.paged_read(d.cu, d.start, d.table, *d.cache(), n_tokens=2 ** 31 - 1)           # 4 TiB
+    for got, want in zip(kvq.paged_read(d.cu, d.start, d.table, *d.cache(), n_tokens=c.n), c.read("fp16")):
+        assert same(got, want)
