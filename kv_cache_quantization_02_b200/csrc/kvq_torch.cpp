@@ -58,7 +58,7 @@ int element_type(at::ScalarType t, const char* name) {
   throw Wrong(std::string(name) + " must be torch.float16 or torch.bfloat16, got " + c10::toString(t));
 }
 
-// The C entry points take 32-bit sizes.
+// The C entry points take 32-bit sizes, and counts of tokens below 2^31.
 int narrow(int64_t x, const char* name) {
   if (x > INT32_MAX) throw Wrong(std::string(name) + " is too large");
   return static_cast<int>(x);
@@ -208,6 +208,7 @@ PyObject* paged_read(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const int64_t tokens = PyLong_AsLongLong(a[7]);
     if (tokens == -1 && PyErr_Occurred()) throw Wrong("");
     if (tokens < 0) throw Wrong("n_tokens must not be negative");
+    narrow(tokens, "n_tokens");                   // before outputs of that size are asked for
     const int dtype = a[8] == Py_True ? KVQ_BF16 : KVQ_FP16;
     const at::ScalarType type = dtype == KVQ_BF16 ? at::kBFloat16 : at::kHalf;
     const int64_t shape[3] = {tokens, c.Hkv, c.D};

@@ -811,3 +811,12 @@ def test_out_of_memory(kvq):
         kvq.paged_read(d.cu, d.start, d.table, *d.cache(), n_tokens=2 ** 31 - 1)           # 4 TiB
     for got, want in zip(kvq.paged_read(d.cu, d.start, d.table, *d.cache(), n_tokens=c.n), c.read("fp16")):
         assert same(got, want)
+
+
+def test_more_tokens_than_a_call_takes(kvq):
+    """2^31 tokens and more are refused by name, not by what their outputs would need."""
+    c = Case(128, 2, 16, "int8", [3], [5], seed=28)
+    d = c.cuda()
+    for n in (2 ** 31, 2 ** 40, 2 ** 62):
+        with pytest.raises(ValueError, match="n_tokens"):
+            kvq.paged_read(d.cu, d.start, d.table, *d.cache(), n_tokens=n)
