@@ -406,7 +406,8 @@ int kvq_paged_read(const int32_t *cu_tokens, const int32_t *start, const int32_t
  * positions; its own key has been written).  No key seen gives zeros.
  *
  *   q           [in]  [B][Hq][D], sequences q_stride apart; Hq a multiple of Hkv.
- *   seq_len     [in]  int32 [B], each in [0, max_blocks * block].
+ *   seq_len     [in]  int32 [B], each in [0, max_blocks * block]; that is at
+ *               most 2^31 - 1024 here.
  *   out         [out] [B][Hq][D], contiguous; must not overlap the inputs.
  *   workspace   scratch for splitting the key axis; 16-byte aligned, at least
  *               kvq_paged_decode_workspace_bytes().  With less, or NULL, the

@@ -314,6 +314,10 @@ int check_shape(int dtype, int format, int B, int max_blocks, int Hkv, int D, in
   return KVQ_OK;
 }
 
+// Attention's positions are ints that are rounded up to whole key tiles, and a warp's lanes go 512 keys on from one's
+// start: the last 1023 below 2^31 are kept free.
+bool fits_positions(int max_blocks, int block) { return static_cast<int64_t>(max_blocks) * block <= INT32_MAX - 1023; }
+
 int check_stride(int64_t stride, int heads, int D) {
   return stride % 8 == 0 && stride >= static_cast<int64_t>(heads) * D && stride <= (int64_t{1} << 40) ? KVQ_OK
                                                                                                    : KVQ_ERR_COUNT;
@@ -479,8 +483,11 @@ int attention_args(AttnArgs& p, const void* q, int dtype, int64_t q_stride, cons
   if (rc != KVQ_OK) return rc;
   p.q = nullptr;
   if (Hq < Hkv || Hq % Hkv != 0 || total_q < 0 || total_q > INT32_MAX || total_q * Hq > INT32_MAX || window < 0 ||
-      !std::isfinite(sm_scale * 1.4426951f))      // (the scale the kernels use)
+      !fits_positions(max_blocks, block) || !std::isfinite(sm_scale * 1.4426951f))      // (the scale the kernels use)
     return KVQ_ERR_COUNT;
+  // a window of the whole table is none; any other reaches back from a query that may stand total_q before its sequence
+  p.window = window < static_cast<int64_t>(max_blocks) * block ? window : 0;
+  if (p.window + total_q > INT32_MAX) return KVQ_ERR_COUNT;
   rc = check_stride(q_stride, Hq, D);
   if (rc != KVQ_OK) return rc;
   if (B == 0 || total_q == 0) return KVQ_OK;
@@ -495,8 +502,6 @@ int attention_args(AttnArgs& p, const void* q, int dtype, int64_t q_stride, cons
   p.cu = cu_q; p.seq_len = seq_len; p.part = nullptr;
   p.q_stride = q_stride; p.total_q = total_q;
   p.R = Hq / Hkv; p.bf16 = dtype == KVQ_BF16; p.negative = sm_scale < 0.0f;
-  // (a window of the whole table is none, and differences with one then fit an int)
-  p.window = window < static_cast<int64_t>(max_blocks) * block ? window : 0;
   p.scale = static_cast<float>(std::fabs(static_cast<double>(sm_scale)) * 1.4426950408889634);
   return KVQ_OK;
 }
@@ -568,7 +573,8 @@ int kvq_paged_read(const int32_t* cu_tokens, const int32_t* start, const int32_t
 static int check_workspace(int B, int max_blocks, int64_t total_q, int Hq, int Hkv, int D, int block, int window) {
   const int rc = check_shape(KVQ_FP16, KVQ_INT8, B, max_blocks, Hkv, D, block, 0);
   if (rc != KVQ_OK) return rc;
-  return Hq < Hkv || Hq % Hkv != 0 || total_q < 0 || total_q > INT32_MAX || total_q * Hq > INT32_MAX || window < 0
+  return Hq < Hkv || Hq % Hkv != 0 || total_q < 0 || total_q > INT32_MAX || total_q * Hq > INT32_MAX || window < 0 ||
+                 !fits_positions(max_blocks, block)
              ? KVQ_ERR_COUNT
              : KVQ_OK;
 }

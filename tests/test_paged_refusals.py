@@ -99,6 +99,29 @@ def test_a_scale_beyond_fp32(kvq):
         assert _attend(kvq, prefill, scale=3e38) == -5 and _attend(kvq, prefill, scale=-3e38) == -5
 
 
+def test_positions_near_two_to_the_31(kvq):
+    """Attention rounds positions up to whole key tiles, and a prompt's first query may stand total_q positions before
+    the sequence: tables and windows for which that leaves an int are refused (q's alignment is looked at after it)."""
+    f = lambda prefill, **kw: _attend(kvq, prefill, q=A + 8, **kw)
+    for block in (16, 32, 64, 128):
+        most = (2 ** 31 - 1024) // block
+        for prefill in (False, True):
+            assert f(prefill, block=block, max_blocks=most, num_blocks=9) == -2
+            assert f(prefill, block=block, max_blocks=most + 1, num_blocks=9) == -5
+        sizes = dict(B=4, Hq=32, Hkv=8, D=128, block=block, window=0)
+        assert kvq.kvq_paged_decode_workspace_bytes(max_blocks=most, **sizes) > 0
+        assert kvq.kvq_paged_decode_workspace_bytes(max_blocks=most + 1, **sizes) == -1
+        assert kvq.kvq_paged_prefill_workspace_bytes(max_blocks=most, total_q=9, **sizes) >= 0
+        assert kvq.kvq_paged_prefill_workspace_bytes(max_blocks=most + 1, total_q=9, **sizes) == -1
+    wide = dict(max_blocks=(2 ** 31 - 1024) // 64, num_blocks=9, Hq=1, Hkv=1, q_stride=128)
+    assert f(True, **wide, n=2 ** 30, window=2 ** 30 - 1) == -2
+    assert f(True, **wide, n=2 ** 30, window=2 ** 30) == -5
+    assert f(True, **wide, n=2 ** 30, window=2 ** 31 - 1) == -2          # (the whole table: none)
+    # the new tokens' write and read have no such rounding
+    assert _write(kvq, k=A + 8, max_blocks=(2 ** 31 - 64) // 64, num_blocks=9) == -2
+    assert _read(kvq, k=A + 8, max_blocks=(2 ** 31 - 64) // 64, num_blocks=9) == -2
+
+
 def test_attention(kvq):
     for prefill in (False, True):
         f = lambda **kw: _attend(kvq, prefill, **kw)
