@@ -345,7 +345,8 @@ int kvq_attention_decode_static(const uint16_t *q, const uint8_t *k_packed,
  *   *_stride elements from one token's row [heads][D] to the next; a multiple
  *            of 8, at least heads * D.
  * Codes, q, k, v and outputs are 16-byte aligned; tables, lengths and scales
- * 4-byte.  num_blocks * Hkv * block < 2^31.  Status order: shape (KVQ_ERR_DIM,
+ * 4-byte.  num_blocks * Hkv * block < 2^31.  A table of no blocks (max_blocks 0)
+ * and a cache of none (num_blocks 0) may be NULL.  Status order: shape (KVQ_ERR_DIM,
  * KVQ_ERR_FORMAT, KVQ_ERR_COUNT), NULL, alignment.
  *
  * Tables and lengths are device memory and are checked on the device: a

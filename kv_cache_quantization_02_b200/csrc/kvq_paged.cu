@@ -301,6 +301,12 @@ __global__ void __launch_bounds__(T) paged_read_kernel(Cache c, Tokens t, uint16
 // Argument checks and launches.
 // ---------------------------------------------------------------------------
 
+// A table without columns and a cache without blocks are never read: they need no address (empty tensors have none).
+bool missing(const void* table, int max_blocks, const void* kc, const void* vc, const void* ks, const void* vs,
+             int64_t num_blocks) {
+  return (!table && max_blocks > 0) || (num_blocks > 0 && (!kc || !vc || !ks || !vs));
+}
+
 bool aligned_to(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 
 int check_shape(int dtype, int format, int B, int max_blocks, int Hkv, int D, int block, int64_t num_blocks) {
@@ -491,11 +497,12 @@ int attention_args(AttnArgs& p, const void* q, int dtype, int64_t q_stride, cons
   rc = check_stride(q_stride, Hq, D);
   if (rc != KVQ_OK) return rc;
   if (B == 0 || total_q == 0) return KVQ_OK;
-  if (!q || !seq_len || !table || !kc || !vc || !ks || !vs || !out) return KVQ_ERR_NULL;
+  if (!q || !seq_len || !out || missing(table, max_blocks, kc, vc, ks, vs, num_blocks)) return KVQ_ERR_NULL;
   if (!aligned_to(q, 16) || !aligned_to(kc, 16) || !aligned_to(vc, 16) || !aligned_to(out, 16) ||
       !aligned_to(seq_len, 4) || !aligned_to(table, 4) || !aligned_to(ks, 4) || !aligned_to(vs, 4) ||
       !aligned_to(cu_q, 4))
     return KVQ_ERR_ALIGN;
+  if (num_blocks == 0) kc = vc = q;               // what copies of no bytes point to (they want an address all the same)
   p.c = make_cache(kc, vc, ks, vs, table, B, max_blocks, Hkv, D, block, num_blocks);
   p.q = static_cast<const uint16_t*>(q);
   p.out = static_cast<uint16_t*>(out);
@@ -530,7 +537,8 @@ int kvq_paged_write(const void* k, const void* v, int dtype, int64_t k_stride, i
   if (n_tokens < 0 || n_tokens > INT32_MAX) return KVQ_ERR_COUNT;
   if (check_stride(k_stride, Hkv, D) != KVQ_OK || check_stride(v_stride, Hkv, D) != KVQ_OK) return KVQ_ERR_COUNT;
   if (B == 0 || n_tokens == 0) return KVQ_OK;
-  if (!k || !v || !cu_tokens || !start || !block_table || !k_codes || !v_codes || !k_scales || !v_scales)
+  if (!k || !v || !cu_tokens || !start ||
+      missing(block_table, max_blocks, k_codes, v_codes, k_scales, v_scales, num_blocks))
     return KVQ_ERR_NULL;
   if (!aligned_to(k, 16) || !aligned_to(v, 16) || !aligned_to(k_codes, 16) || !aligned_to(v_codes, 16) ||
       !aligned_to(cu_tokens, 4) || !aligned_to(start, 4) || !aligned_to(block_table, 4) || !aligned_to(k_scales, 4) ||
@@ -554,7 +562,8 @@ int kvq_paged_read(const int32_t* cu_tokens, const int32_t* start, const int32_t
   if (rc != KVQ_OK) return rc;
   if (n_tokens < 0 || n_tokens > INT32_MAX) return KVQ_ERR_COUNT;
   if (B == 0 || n_tokens == 0) return KVQ_OK;
-  if (!cu_tokens || !start || !block_table || !k_codes || !v_codes || !k_scales || !v_scales || !k_out || !v_out)
+  if (!cu_tokens || !start || !k_out || !v_out ||
+      missing(block_table, max_blocks, k_codes, v_codes, k_scales, v_scales, num_blocks))
     return KVQ_ERR_NULL;
   if (!aligned_to(k_out, 16) || !aligned_to(v_out, 16) || !aligned_to(k_codes, 16) || !aligned_to(v_codes, 16) ||
       !aligned_to(cu_tokens, 4) || !aligned_to(start, 4) || !aligned_to(block_table, 4) || !aligned_to(k_scales, 4) ||

@@ -820,3 +820,39 @@ def test_more_tokens_than_a_call_takes(kvq):
     for n in (2 ** 31, 2 ** 40, 2 ** 62):
         with pytest.raises(ValueError, match="n_tokens"):
             kvq.paged_read(d.cu, d.start, d.table, *d.cache(), n_tokens=n)
+
+
+def _empty_cache(num_blocks, fmt):
+    return (*(torch.zeros((num_blocks, 2, 16, 128), dtype=FORMATS[fmt], device="cuda") for _ in range(2)),
+            *(torch.ones((num_blocks, 2), device="cuda") for _ in range(2)))
+
+
+@pytest.mark.parametrize("fmt", ["int8", "e4m3"])
+@pytest.mark.parametrize("B", [3, 40])
+def test_tables_without_columns(kvq, B, fmt):
+    """Sequences that have no block yet, in a cache with and without blocks: nothing is seen, and nothing reported."""
+    table = torch.zeros((B, 0), dtype=torch.int32, device="cuda")
+    zero = torch.zeros(B, dtype=torch.int32, device="cuda")
+    cu = torch.zeros(B + 1, dtype=torch.int32, device="cuda")
+    one = torch.arange(B + 1, dtype=torch.int32, device="cuda")
+    x, q = (torch.ones((B, h, 128), dtype=torch.float16, device="cuda") for h in (2, 6))
+    for num_blocks in (5, 0):
+        cache = _empty_cache(num_blocks, fmt)
+        kvq.paged_write(x, x, cu, zero, table, *cache)
+        k, v = kvq.paged_read(cu, zero, table, *cache, n_tokens=2, k_out=x[:2].clone(), v_out=x[:2].clone())
+        assert bool((k == 1).all()) and bool((v == 1).all())
+        for ws in (True, False):
+            assert not kvq.paged_attention_decode(q, zero, table, *cache, sm_scale=1.0, workspace=ws).any()
+            assert not kvq.paged_attention_prefill(q, one, zero, table, *cache, sm_scale=1.0, workspace=ws).any()
+    # tokens and lengths that the table has no room for are reported
+    kvq.paged_write(x, x, one, zero, table, *cache)
+    assert kvq.kvq_fault_status(clear=True) == 4
+    assert not kvq.paged_attention_decode(q, zero + 1, table, *cache, sm_scale=1.0).any()
+    assert kvq.kvq_fault_status(clear=True) == 8
+    # and so is a table whose blocks the cache has not
+    table = torch.zeros((B, 300), dtype=torch.int32, device="cuda")
+    for ws in (True, False):
+        assert not kvq.paged_attention_decode(q, zero + 4700, table, *cache, sm_scale=1.0, workspace=ws).any()
+        assert kvq.kvq_fault_status(clear=True) == 4
+        assert not kvq.paged_attention_prefill(q, one, zero + 4700, table, *cache, sm_scale=1.0, workspace=ws).any()
+        assert kvq.kvq_fault_status(clear=True) == 4

@@ -122,6 +122,19 @@ def test_positions_near_two_to_the_31(kvq):
     assert _read(kvq, k=A + 8, max_blocks=(2 ** 31 - 64) // 64, num_blocks=9) == -2
 
 
+def test_empty_tables_and_caches(kvq):
+    """Empty tensors have no address: a table without columns needs none, nor does a cache without blocks (q's or k's
+    alignment is looked at after that)."""
+    calls = [lambda **kw: _write(kvq, k=A + 8, **kw), lambda **kw: _read(kvq, k=A + 8, **kw),
+             lambda **kw: _attend(kvq, False, q=A + 8, **kw), lambda **kw: _attend(kvq, True, q=A + 8, **kw)]
+    for f in calls:
+        assert f(max_blocks=0, table=0) == -2
+        assert f(num_blocks=0, kc=0, vc=0, ks=0, vs=0) == -2
+        assert f(max_blocks=0, num_blocks=0, table=0, kc=0, vc=0, ks=0, vs=0) == -2
+        assert f(table=0) == -1 and f(kc=0) == -1 and f(vs=0) == -1
+        assert f(max_blocks=0, table=0, kc=0) == -1 and f(num_blocks=0, kc=0, vc=0, ks=0, vs=0, table=0) == -1
+
+
 def test_attention(kvq):
     for prefill in (False, True):
         f = lambda **kw: _attend(kvq, prefill, **kw)
