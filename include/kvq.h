@@ -68,7 +68,9 @@ typedef enum {
     KVQ_ERR_ALIGN = -2,   /* a pointer violates its alignment requirement  */
     KVQ_ERR_DIM = -3,     /* D is not 64, 128 or 256                        */
     KVQ_ERR_GROUP = -4,   /* group is not a power of two in [16, D]         */
-    KVQ_ERR_COUNT = -5,   /* n_vec < 0 or n_vec > 2^31 - 256                */
+    KVQ_ERR_COUNT = -5,   /* n_vec < 0 or n_vec > 2^31 - 256; attention and
+                             paged cache: a count, size, stride, window or
+                             softmax scale out of range                     */
     KVQ_ERR_LAUNCH = -6,  /* the kernel launch failed (see kvq_last_cuda_error) */
     KVQ_ERR_FORMAT = -7   /* paged cache: unknown block size, code format or
                              element type                                  */

@@ -1455,7 +1455,7 @@ const char* kvq_status_string(int status) {
     case KVQ_ERR_ALIGN: return "KVQ_ERR_ALIGN: a pointer is misaligned";
     case KVQ_ERR_DIM: return "KVQ_ERR_DIM: D must be 64, 128 or 256";
     case KVQ_ERR_GROUP: return "KVQ_ERR_GROUP: group must be a power of two in [16, D]";
-    case KVQ_ERR_COUNT: return "KVQ_ERR_COUNT: n_vec must be in [0, 2^31 - 256]";
+    case KVQ_ERR_COUNT: return "KVQ_ERR_COUNT: a count, size, stride, window or softmax scale is out of range (n_vec: [0, 2^31 - 256])";
     case KVQ_ERR_LAUNCH: return "KVQ_ERR_LAUNCH: the kernel launch failed";
     case KVQ_ERR_FORMAT: return "KVQ_ERR_FORMAT: unknown block size, code format or element type";
     default: return "unknown kvq status";

@@ -160,6 +160,12 @@ def test_workspace_shapes(kvq):
     assert kvq.kvq_status_string(-7).startswith("KVQ_ERR_FORMAT")
 
 
+def test_what_the_statuses_say(kvq):
+    """KVQ_ERR_COUNT is more than the codec's number of vectors: a window, a stride, a softmax scale, ..."""
+    text = str(kvq.KvqError(_attend(kvq, False, window=-1)))
+    assert text.startswith("KVQ_ERR_COUNT") and "window" in text and "n_vec" in text
+
+
 def test_binding_checks(kvq):
     """The torch wrappers name the argument that is wrong, before the library is called."""
     c = Case(128, 2, 16, "int8", [3, 4], [5, 6], seed=1)
