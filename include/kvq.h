@@ -341,7 +341,8 @@ int kvq_attention_decode_static(const uint16_t *q, const uint8_t *k_packed,
  *   dtype    element type of q, k, v and outputs: KVQ_FP16 or KVQ_BF16.
  *   format   KVQ_INT8: two's-complement codes in [-127, 127]; KVQ_E4M3: OCP
  *            8-bit floats (4 exponent bits, largest 448; the NaN pattern is
- *            never written, and reads as +-480 or NaN).
+ *            never written, and reads as NaN; attention that meets it at a
+ *            visible position gives NaN, in other rows of the sequence too).
  *   block    tokens per cache block: 16, 32, 64 or 128.
  *   D        64, 128 or 256.
  *   *_stride elements from one token's row [heads][D] to the next; a multiple
@@ -417,7 +418,9 @@ int kvq_paged_read(const int32_t *cu_tokens, const int32_t *start, const int32_t
  *               call runs unsplit: same result up to fp32 summation order,
  *               slower.  Calls that may overlap in time need one each.
  * The codes enter the products exactly, scores and sums are fp32, the softmax
- * weights are fp16 values (relative rounding 2^-11) in the value product.
+ * weights are fp16 values in the value product alone: each weight times its
+ * value scale is off by 2^-11 of itself or, where it is below 2^-20 of the
+ * row's largest such product, by up to 2^-31 of that one.
  * Key and value scales are read as max(scale, 2^-40), a NaN as 2^-40.
  */
 int kvq_paged_attention_decode(const void *q, int dtype, int64_t q_stride, const int32_t *seq_len,

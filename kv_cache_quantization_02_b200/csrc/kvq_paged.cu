@@ -198,7 +198,12 @@ __global__ void __launch_bounds__(T, 512 / T) paged_write_kernel(Cache c, Tokens
 // The same with a warp per item, for calls of about a token per sequence (at most
 // two): four times fewer thread blocks, and no barrier.  64 tokens of 8 heads
 // took 2.7 us, 7.1 us with a thread block of 128 an item.  The first 32 units stay in
-// registers (two tokens at D = 256), any others are read again.
+// registers (two tokens at D = 256), any others are read again.  Both sides of the
+// rule at its border (blocks of 64 tokens, D = 128, 8 heads): two tokens for each of 64
+// sequences 3.1 us, a thread block an item 6.0; of 256 sequences 5.0 and 15.2.  Where one of
+// them has all the tokens but one each: 7.0 and 6.0 us; 7.6 and 15.3.  Codes that are rounded
+// again come on top: 64 tokens whose blocks' scales all grow take 6.1 us, not 2.7 (D = 128,
+// blocks of 64), at D = 256 and blocks of 128 12.9 us.
 template <int FMT, bool BF16>
 __device__ __forceinline__ float largest(uint4 w) {
   const uint32_t v[4] = {w.x, w.y, w.z, w.w};

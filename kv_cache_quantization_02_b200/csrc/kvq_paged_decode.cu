@@ -2,7 +2,10 @@
 // 8-bit cache (include/kvq.h, kvq_paged_attention_decode); the softmax's form
 // is in kvq_paged_attn.cuh.
 //
-// Bound: the codes of K and V, read once (2 D bytes a key and KV head).
+// Bound: the codes of K and V (2 D bytes a key and KV head), read once for every
+// 8 query heads of a KV head.  With more they are streamed again: 64 ragged
+// sequences of up to 4K tokens, D = 128, 4 KV heads, take 58 us with 12 or 16 query
+// heads on each, where reading them once would take 24.
 //
 // Work.  The 32-key tiles of all (sequence, KV head, up to 8 query heads) form
 // one line, and every thread block takes an equal stretch of it, so ragged

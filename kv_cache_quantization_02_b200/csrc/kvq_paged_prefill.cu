@@ -30,8 +30,10 @@
 // The reference of a row's softmax moves rarely (kLazy), and only then is O
 // rescaled in tensor memory, by the thread that owns the row.
 //
-// Measured at D = 128, 32 query heads on 8: a prompt of 8192 tokens 0.60 ms (916
-// TFLOP/s), of 16384 (16 on 4) 1030; 8 x 32 tokens behind 8192 74 us.  A key tile takes 4,150 cycles: 2,048 of the
+// Measured at D = 128, 32 query heads on 8: a prompt of 8192 tokens 0.60 ms a call (911
+// TFLOP/s; 586 us on the device), of 16384 (16 on 4) 1.10-1.13 ms (974-996); 8 x 32 tokens
+// behind 8192 74-76 us.  8192 tokens at D = 64: 550 us (500 TFLOP/s), at D = 256 (16 on 4)
+// 650 us (845).  A key tile (D = 128) takes 4,150 cycles: 2,048 of the
 // exponential unit, about 2,500 of the tensor cores, the rest latencies.  With
 // one score buffer of 128 keys for each 128 rows (larger MMAs, but the softmax
 // waits for them) it was 0.72 ms, with sixteen softmax warps 0.64 ms.
