@@ -856,3 +856,57 @@ def test_tables_without_columns(kvq, B, fmt):
         assert kvq.kvq_fault_status(clear=True) == 4
         assert not kvq.paged_attention_prefill(q, one, zero + 4700, table, *cache, sm_scale=1.0, workspace=ws).any()
         assert kvq.kvq_fault_status(clear=True) == 4
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("part", ["k", "v"])
+def test_the_nan_pattern(kvq, D, part):
+    """e4m3's NaN pattern, which no write makes, reads as NaN; in attention it stays in its sequence and KV head."""
+    c = Case(D, 2, 16, "e4m3", [40, 330], [3, 4], seed=30, R=2)
+    page = int(c.table[0, 1])
+    (c.kc if part == "k" else c.vc).view(torch.uint8)[page, 0, 5, 7] = 0xFF       # position 21, head 0, channel 7
+    d = c.cuda()
+    q = c.rows(4, "fp16")
+    every = torch.tensor([0, 43, 377], dtype=torch.int32, device="cuda")
+    got = kvq.paged_read(every, torch.zeros_like(d.start), d.table, *d.cache(), n_tokens=377)
+    for x, name in zip(got, "kv"):
+        assert x.isnan().nonzero().tolist() == ([[21, 0, 7]] if name == part else [])
+    clean = (c.kc if part == "k" else c.vc).view(torch.uint8)
+    clean[page, 0, 5, 7] = 0
+    for ws in (True, False):
+        want, bound = c.attend(q, c.cu, c.seq_len, 0.1)
+        out = kvq.paged_attention_prefill(q.cuda(), d.cu, d.seq_len, d.table, *d.cache(), sm_scale=0.1, workspace=ws)
+        hit = out[:3, :2] if part == "k" else out[:3, :2, 7]
+        assert hit.isnan().all()
+        check(out[:3, 2:], want[:3, 2:], bound[:3, 2:])
+        check(out[3:], want[3:], bound[3:])
+        want, bound = c.attend(q[2:4], range(3), c.seq_len, 0.1)
+        out = kvq.paged_attention_decode(q[2:4].cuda(), d.seq_len, d.table, *d.cache(), sm_scale=0.1, workspace=ws)
+        assert (out[0, :2] if part == "k" else out[0, :2, 7]).isnan().all()
+        check(out[0, 2:], want[0, 2:], bound[0, 2:])
+        check(out[1], want[1], bound[1])
+
+
+def test_prompts_on_two_streams_at_once(kvq):
+    """Split prompt calls, each with the workspace that it allocates, and a write beside them, give what each gives
+    alone."""
+    c = Case(128, 2, 32, "int8", [4000, 900], [20, 70], seed=31, R=4)
+    e = Case(128, 2, 32, "int8", [10, 30], [50, 9], seed=32)
+    d, f = c.cuda(), e.cuda()
+    qs = [c.rows(8, "bf16").cuda() for _ in range(2)]
+    k = e.rows(2, "fp16")
+    run = lambda q, **kw: kvq.paged_attention_prefill(q, d.cu, d.seq_len, d.table, *d.cache(), sm_scale=0.1, **kw)
+    assert kvq.kvq_paged_prefill_workspace_bytes(2, c.table.shape[1], c.n, 8, 2, 128, 32) > 0
+    alone, k_gpu = [run(q) for q in qs], k.cuda()
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(3)]
+    outs = [[], []]
+    for _ in range(20):
+        for i in range(2):
+            outs[i].append(run(qs[i], stream=streams[i]))
+        kvq.paged_write(k_gpu, k_gpu, f.cu, f.start, f.table, *f.cache(), stream=streams[2])
+    torch.cuda.synchronize()
+    for i in range(2):
+        assert all(same(o, alone[i]) for o in outs[i])
+    e.write(k, k)
+    assert same_cache(e, f)
